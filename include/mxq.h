@@ -44,6 +44,7 @@
  *      MXFP4 scales : uint8 [rows x ld_scales], one E8M0 byte per 32-element block
  *                     along the row; value 2^(byte - 127).
  *      FP8          : uint8 [rows x ld], OCP E4M3.
+ *      int8         : two's complement codes, one binary32 scale for each row.
  *      bf16         : uint16 bit patterns.
  *    The quantizer's output is exactly the GEMMs' input: there is no hidden reshuffle.
  *    GEMM weights W are N x K with K contiguous (nn.Linear layout); out = A * W^T.
@@ -304,6 +305,121 @@ mxq_status mxq_dequantize(const uint8_t* codes, int64_t ld_codes, const uint8_t*
  */
 mxq_status mxq_dequantize_fp8(const uint8_t* q, int64_t ld_q, float a_scale, int64_t rows, int64_t cols,
                               uint16_t* y, int64_t ld_y, void* stream);
+
+/*
+ * 8-bit integers: one binary32 scale for each row (a token of the activations, an output
+ * channel of the weights), for layers that need more than W4A4 and no calibration.
+ *
+ * mxq_quantize_int8 -- symmetric 8-bit quantization of each row:
+ *   amax = max |x| of the row;  scale = fl32(amax / 127),  inv = fl32(127 / amax);
+ *   code = RNE(fl32(x * inv)), in [-127, 127]; both quotients correctly rounded.
+ * A row whose amax is below 2^-118 (an all-zero row too) gets scale 0 and codes 0.  A row
+ * holding an infinity or a NaN gets scale NaN and codes 0; other rows are unaffected.
+ * x      : rows x cols of `dt`, pitch ld_x elements; base and pitch 16-byte aligned.
+ * codes  : out, rows x cols int8, pitch ld_codes bytes; base and pitch multiples of 16.
+ * scales : out, float[rows].
+ * cols % 16 == 0 (cols == 0 writes scales of 0).  Errors as for mxq_quantize_fp8.
+ */
+mxq_status mxq_quantize_int8(const void* x, mxq_dtype dt, int64_t rows, int64_t cols, int64_t ld_x,
+                             int8_t* codes, int64_t ld_codes, float* scales, void* stream);
+
+/*
+ * mxq_dequantize_int8 -- 8-bit codes -> bf16: y = bf16_RNE( fl32( code * scale[row] ) ), the
+ * quantize-dequantize (QDQ) emulation step.
+ * codes : rows x cols int8, pitch ld_codes bytes (base and pitch multiples of 8);
+ * scales: float[rows];  y : out, rows x cols bf16, pitch ld_y elements, base 16-byte
+ * aligned, ld_y % 8 == 0.  cols % 8 == 0.
+ */
+mxq_status mxq_dequantize_int8(const int8_t* codes, int64_t ld_codes, const float* scales, int64_t rows,
+                               int64_t cols, uint16_t* y, int64_t ld_y, void* stream);
+
+/*
+ * mxq_gemm_w8a8 -- 8-bit product with a scale for each token and each output channel:
+ *   acc = sum_k a[m,k] * w[n,k] (int32, exact);  t = fl32( fl32(acc) * a_scales[m] );
+ *   v = fl32( t * w_scales[n] ), or with a bias the fused multiply-add t * w_scales[n] + bias[n]
+ *   rounded once;  out = v as binary32 (MXQ_F32) or bf16_RNE(v) (MXQ_BF16).
+ * a : M x K int8, pitch ld_a bytes; w : N x K int8, pitch ld_w bytes.  Bases and pitches
+ *     multiples of 16, pitches below 2^23.  Any int8 codes, -128 included.
+ * a_scales, w_scales : float, element m (n) at m * inc_as (n * inc_ws), increments >= 0 (0:
+ *     one scale for all).  bias : float[N] or NULL.
+ * out : M x N of out_dt, pitch ld_out elements (>= N), naturally aligned.
+ * K % 16 == 0 and K < 2^17 (the sum then fits int32); K == 0 gives the bias, or zeros.
+ */
+mxq_status mxq_gemm_w8a8(const int8_t* a, int64_t ld_a, const float* a_scales, int64_t inc_as,
+                         const int8_t* w, int64_t ld_w, const float* w_scales, int64_t inc_ws,
+                         const float* bias, int64_t M, int64_t N, int64_t K, void* out,
+                         mxq_dtype out_dt, int64_t ld_out, void* stream);
+
+/*
+ * mxq_gemm_w8a8_fused -- mxq_gemm_w8a8 on unquantized activations, equal bit for bit to
+ * mxq_quantize_int8(a) followed by mxq_gemm_w8a8 on the result.
+ * a : M x K of `dt`, pitch ld_a elements; base and pitch (bytes) 16-byte aligned.
+ * workspace, ws_bytes : device memory of at least mxq_gemm_w8a8_fused_workspace_bytes(M, N, K)
+ *     bytes, 16-byte aligned (NULL where that is 0), owned by the caller and not used by
+ *     anything else until the call's work on `stream` is done.
+ * The other arguments and errors are those of mxq_quantize_int8 and mxq_gemm_w8a8;
+ * MXQ_ERR_INVALID_ARG for a missing, misaligned or short workspace.
+ */
+mxq_status mxq_gemm_w8a8_fused(const void* a, mxq_dtype dt, int64_t ld_a, const int8_t* w, int64_t ld_w,
+                               const float* w_scales, int64_t inc_ws, const float* bias, int64_t M,
+                               int64_t N, int64_t K, void* out, mxq_dtype out_dt, int64_t ld_out,
+                               void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * mxq_gemm_w8a8_fused_workspace_bytes -- workspace of mxq_gemm_w8a8_fused for a shape (0 for
+ * an empty or invalid one).  Host only; no device work.
+ */
+size_t mxq_gemm_w8a8_fused_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* Which elements of a head turn together (mxq_qk_norm_rope), R the rotated width. */
+typedef enum {
+  MXQ_ROPE_INTERLEAVED = 0, /* (2i, 2i+1), i < R/2 */
+  MXQ_ROPE_HALVES = 1,      /* (i, i + R/2), i < R/2 */
+  MXQ_ROPE_STYLE_MAX_ENUM = 0x7FFFFFFF
+} mxq_rope_style;
+
+/*
+ * mxq_qk_norm_rope -- root-mean-square norm of every query and key head with the position
+ * rotation in the same pass (the step between the QKV projection and attention in FLUX- and
+ * Wan-like blocks).  For each token and head x of head_dim elements, in binary32:
+ *   r = 1 / sqrt( sum x^2 / head_dim + eps );  y = (x * r) * w;
+ *   pairs (a, b) of the first rot_dim elements -> (a c - b s, b c + a s), c and s from row
+ *   p of cos and sin, column i (mxq_rope_style), p = positions[token] (token if NULL);
+ * rounded to `dt` once.  The sum of squares is formed in binary32: a head where it
+ * overflows comes out as zeros.  The rotated elements of a token whose position is outside
+ * [0, table_rows) come out as NaN, and no memory outside the table is read for it.
+ * q, k    : tokens x heads x head_dim of `dt`; element (t, h, d) at t * ld + h * hs + d.
+ *           Either may have 0 heads (its other arguments are then ignored).
+ * w_q, w_k: head_dim weights of w_dt each, or NULL for 1.
+ * cos, sin: table_rows x rot_dim / 2 float, pitch ld_table; unused when rot_dim == 0.
+ * out_q, out_k : like q and k, of `dt`.  An output may be its input with the same pitches;
+ *           no other overlap.
+ * head_dim: a multiple of 8 up to 512; rot_dim: a multiple of 8 up to head_dim; heads up
+ *           to 65536 each.  Bases 16-byte aligned; all pitches of q, k, out_q, out_k
+ *           multiples of 16 bytes and not negative; ld_table % 4 == 0.
+ */
+mxq_status mxq_qk_norm_rope(const void* q, int64_t heads_q, int64_t ld_q, int64_t hs_q, const void* k,
+                            int64_t heads_k, int64_t ld_k, int64_t hs_k, mxq_dtype dt, int64_t tokens,
+                            int64_t head_dim, const void* w_q, const void* w_k, mxq_dtype w_dt, float eps,
+                            const float* cos, const float* sin, int64_t ld_table, int64_t table_rows,
+                            int64_t rot_dim, const int64_t* positions, mxq_rope_style style, void* out_q,
+                            int64_t ld_oq, int64_t hs_oq, void* out_k, int64_t ld_ok, int64_t hs_ok,
+                            void* stream);
+
+/*
+ * mxq_quantize_qk_norm_rope -- the same, then the rule of mxq_quantize_int8 on the binary32
+ * values of each token and head: codes int8 (pitches in bytes, bases and pitches multiples
+ * of 8) and one scale for each, at t * ld_s + h.  With pitches that are multiples of 16 a head's codes are
+ * operands of mxq_gemm_w8a8 (the 8-bit score product of a head).
+ */
+mxq_status mxq_quantize_qk_norm_rope(const void* q, int64_t heads_q, int64_t ld_q, int64_t hs_q, const void* k,
+                                     int64_t heads_k, int64_t ld_k, int64_t hs_k, mxq_dtype dt, int64_t tokens,
+                                     int64_t head_dim, const void* w_q, const void* w_k, mxq_dtype w_dt, float eps,
+                                     const float* cos, const float* sin, int64_t ld_table, int64_t table_rows,
+                                     int64_t rot_dim, const int64_t* positions, mxq_rope_style style,
+                                     int8_t* codes_q, int64_t ld_cq, int64_t hs_cq, float* scales_q, int64_t ld_sq,
+                                     int8_t* codes_k, int64_t ld_ck, int64_t hs_ck, float* scales_k, int64_t ld_sk,
+                                     void* stream);
 
 /*
  * Measurement aid (not part of the quantize / GEMM path).

@@ -9,7 +9,8 @@ built (``python mxfp4_microscaled_quantization_amd/build.py``); there is no fall
 
 Function names mirror the C entry points without the ``mxq_`` prefix:
 ``quantize``, ``quantize_fp8``, ``absmax``, ``gemm_w4a4``, ``gemm_w4a4_fused``, ``gemm_w4a8``, ``gemm_bf16``,
-``sqnr``, ``dequantize``, ``dequantize_fp8``, ``fp8_static_scales``.  ``lib`` exposes the raw ctypes functions.
+``sqnr``, ``dequantize``, ``dequantize_fp8``, ``fp8_static_scales``, ``quantize_int8``, ``dequantize_int8``, ``gemm_w8a8``,
+``gemm_w8a8_fused``, ``qk_norm_rope``, ``quantize_qk_norm_rope``.  ``lib`` exposes the raw ctypes functions.
 """
 
 import ctypes
@@ -20,7 +21,8 @@ import torch
 __all__ = [
     "lib", "MxqError", "quantize", "quantize_into", "quantize_hadamard", "SCALE_RULES", "quantize_fp8", "absmax", "fp8_static_scales",
     "gemm_w4a4", "gemm_w4a4_fused", "gemm_w4a8", "gemm_bf16", "sqnr", "sqnr_noalloc", "sqnr_workspace_bytes", "dequantize", "dequantize_fp8",
-    "mfma_ceiling", "MFMA_FLOP", "check_buffer",
+    "quantize_int8", "dequantize_int8", "gemm_w8a8", "gemm_w8a8_fused", "w8a8_fused_workspace_bytes",
+    "qk_norm_rope", "quantize_qk_norm_rope", "ROPE_STYLES", "mfma_ceiling", "MFMA_FLOP", "check_buffer",
     "LIB_PATH", "ABI_SYMBOLS", "ABI_VERSION",
 ]
 
@@ -33,6 +35,10 @@ MXQ_OK, MXQ_ERR_INVALID_ARG, MXQ_ERR_UNSUPPORTED, MXQ_ERR_HIP = 0, 1, 2, 3
 MXQ_F32, MXQ_BF16 = 0, 1
 
 _i64, _ptr, _f32, _sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_size_t
+
+# q and k (pointer, heads, pitches), dt, tokens, head_dim, weights, w_dt, eps, tables, rot_dim, positions, style
+_QK_ARGS = [_ptr, _i64, _i64, _i64, _ptr, _i64, _i64, _i64, ctypes.c_int, _i64, _i64, _ptr, _ptr, ctypes.c_int, _f32,
+            _ptr, _ptr, _i64, _i64, _i64, _ptr, ctypes.c_int]
 
 #: every exported symbol with (restype, argtypes) -- the C ABI of include/mxq.h
 ABI_SYMBOLS = {
@@ -57,6 +63,15 @@ ABI_SYMBOLS = {
     "mxq_fp8_static_scales": (ctypes.c_int, [_f32, ctypes.POINTER(_f32), ctypes.POINTER(_f32)]),
     "mxq_mfma_ceiling": (ctypes.c_int, [ctypes.c_int, _ptr, _ptr, _ptr, _ptr, _i64, _i64, _i64, _i64, _i64, _ptr,
                                         _ptr]),
+    "mxq_quantize_int8": (ctypes.c_int, [_ptr, ctypes.c_int, _i64, _i64, _i64, _ptr, _i64, _ptr, _ptr]),
+    "mxq_dequantize_int8": (ctypes.c_int, [_ptr, _i64, _ptr, _i64, _i64, _ptr, _i64, _ptr]),
+    "mxq_gemm_w8a8": (ctypes.c_int, [_ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _i64, _i64, _ptr,
+                                     ctypes.c_int, _i64, _ptr]),
+    "mxq_gemm_w8a8_fused": (ctypes.c_int, [_ptr, ctypes.c_int, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _i64, _i64,
+                                           _ptr, ctypes.c_int, _i64, _ptr, _sz, _ptr]),
+    "mxq_gemm_w8a8_fused_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "mxq_qk_norm_rope": (ctypes.c_int, _QK_ARGS + [_ptr, _i64, _i64, _ptr, _i64, _i64, _ptr]),
+    "mxq_quantize_qk_norm_rope": (ctypes.c_int, _QK_ARGS + [_ptr, _i64, _i64, _ptr, _i64] * 2 + [_ptr]),
     "mxq_last_error": (ctypes.c_char_p, []),
     "mxq_abi_version": (ctypes.c_int, []),
 }
@@ -431,3 +446,234 @@ def dequantize_fp8(q, a_scale: float, out=None) -> torch.Tensor:
     ld = check_buffer(out, "out", torch.bfloat16, (R, K), q.device)
     _check(lib.mxq_dequantize_fp8(_p(q), ldq, float(a_scale), R, K, _p(out), ld, _stream()))
     return out
+
+
+# ---------------------------------------------------------------------------------
+# 8-bit integers.  These entry points launch on the tensors' own device, whichever is current.
+
+def _call(fn, device, *args):
+    """``fn(*args, stream)`` with torch's current stream of ``device``, checked."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)))
+
+
+def _matrix(t, name, dtype, device=None, shape=None):
+    """A 2-D GPU tensor of ``dtype`` (or one of several) with contiguous rows: its row pitch."""
+    _dev(t, name, device)
+    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+        raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.stride(0) if rows > 1 else cols
+
+
+def _vector(t, name, n, device, dtype=torch.float32):
+    """A 1-D GPU tensor of ``n`` elements: the distance between them (0 for an expanded one)."""
+    _dev(t, name, device)
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name} must have shape ({n},) (got {tuple(t.shape)})")
+    return t.stride(0) if n > 1 else 1
+
+
+def _flat(t, name, n, device, dtype=torch.float32):
+    if _vector(t, name, n, device, dtype) != 1:
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+_FLOATS = (torch.bfloat16, torch.float32)
+
+
+def quantize_int8(x, codes=None, scales=None):
+    """Symmetric 8-bit codes of the rows of ``x`` (bf16 or fp32 [R, K], K % 16 == 0) with one scale for each:
+    s = fl32(amax / 127), q = RNE(fl32(x * fl32(127 / amax))).  For activations the rows are tokens, for weights
+    output channels.  Returns (codes int8 [R, K], scales float32 [R]), the ones given where they are."""
+    ld = _matrix(x, "x", _FLOATS)
+    R, K = x.shape
+    if codes is None:
+        codes, ldc = torch.empty((R, K), dtype=torch.int8, device=x.device), K
+    else:
+        ldc = _matrix(codes, "codes", torch.int8, x.device, (R, K))
+    if scales is None:
+        scales = torch.empty(R, dtype=torch.float32, device=x.device)
+    else:
+        _flat(scales, "scales", R, x.device)
+    _call(lib.mxq_quantize_int8, x.device, x.data_ptr(), _dtype_code(x), R, K, ld, codes.data_ptr(), ldc,
+          scales.data_ptr())
+    return codes, scales
+
+
+def dequantize_int8(codes, scales, out=None):
+    """8-bit codes [R, K] and scales [R] -> bf16 [R, K]: bf16(fl32(code * scale)) (into ``out`` if given)."""
+    ldc = _matrix(codes, "codes", torch.int8)
+    R, K = codes.shape
+    _flat(scales, "scales", R, codes.device)
+    if out is None:
+        out, ld = torch.empty((R, K), dtype=torch.bfloat16, device=codes.device), K
+    else:
+        ld = _matrix(out, "out", torch.bfloat16, codes.device, (R, K))
+    _call(lib.mxq_dequantize_int8, codes.device, codes.data_ptr(), ldc, scales.data_ptr(), R, K, out.data_ptr(), ld)
+    return out
+
+
+def _w8_out(M, N, device, out, out_dtype):
+    if out is None:
+        if out_dtype not in _FLOATS:
+            raise ValueError("out_dtype must be bfloat16 or float32")
+        return torch.empty((M, N), dtype=out_dtype, device=device), N
+    return out, _matrix(out, "out", _FLOATS, device, (M, N))
+
+
+def gemm_w8a8(a_codes, a_scales, w_codes, w_scales, bias=None, out=None, out_dtype=torch.bfloat16):
+    """8-bit A [M, K] x W [N, K]^T with a scale for each token and channel -> bf16 or fp32 [M, N]:
+    (sum in int32) * a_scales[m] * w_scales[n] + bias[n].  Rows may be strided, scales too (or expanded from one
+    value); ``out`` decides the output type where it is given."""
+    lda = _matrix(a_codes, "a_codes", torch.int8)
+    dev = a_codes.device
+    M, K = a_codes.shape
+    inc_a = _vector(a_scales, "a_scales", M, dev)
+    ldw = _matrix(w_codes, "w_codes", torch.int8, dev)
+    N = w_codes.shape[0]
+    if w_codes.shape[1] != K:
+        raise ValueError(f"w_codes must have {K} columns (got {w_codes.shape[1]})")
+    inc_w = _vector(w_scales, "w_scales", N, dev)
+    if bias is not None:
+        _flat(bias, "bias", N, dev)
+    out, ld = _w8_out(M, N, dev, out, out_dtype)
+    _call(lib.mxq_gemm_w8a8, dev, a_codes.data_ptr(), lda, a_scales.data_ptr(), inc_a, w_codes.data_ptr(), ldw,
+          w_scales.data_ptr(), inc_w, _opt(bias), M, N, K, out.data_ptr(), _dtype_code(out), ld)
+    return out
+
+
+def w8a8_fused_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Workspace bytes of gemm_w8a8_fused for a shape."""
+    return int(lib.mxq_gemm_w8a8_fused_workspace_bytes(M, N, K))
+
+
+def gemm_w8a8_fused(a, w_codes, w_scales, bias=None, out=None, out_dtype=torch.bfloat16):
+    """gemm_w8a8 of unquantized activations A [M, K] (bf16 or fp32, rows may be strided): equal, bit for bit, to
+    gemm_w8a8(*quantize_int8(a), w_codes, w_scales, bias)."""
+    lda = _matrix(a, "a", _FLOATS)
+    dev = a.device
+    M, K = a.shape
+    ldw = _matrix(w_codes, "w_codes", torch.int8, dev)
+    N = w_codes.shape[0]
+    if w_codes.shape[1] != K:
+        raise ValueError(f"w_codes must have {K} columns (got {w_codes.shape[1]})")
+    inc_w = _vector(w_scales, "w_scales", N, dev)
+    if bias is not None:
+        _flat(bias, "bias", N, dev)
+    out, ld = _w8_out(M, N, dev, out, out_dtype)
+    nbytes = lib.mxq_gemm_w8a8_fused_workspace_bytes(M, N, K)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    _call(lib.mxq_gemm_w8a8_fused, dev, a.data_ptr(), _dtype_code(a), lda, w_codes.data_ptr(), ldw,
+          w_scales.data_ptr(), inc_w, _opt(bias), M, N, K, out.data_ptr(), _dtype_code(out), ld, _opt(ws), nbytes)
+    return out
+
+
+ROPE_STYLES = {"interleaved": 0, "halves": 1}
+
+
+def _heads(t, name, dtype=None, device=None, shape=None):
+    """A 3-D GPU tensor [tokens, heads, head_dim] with contiguous heads: (token pitch, head pitch)."""
+    _dev(t, name, device)
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be 3-D [tokens, heads, head_dim]")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    T, H, D = t.shape
+    if D > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must have contiguous heads")
+    hs = t.stride(1) if H > 1 else D
+    return (t.stride(0) if T > 1 else H * hs), hs
+
+
+def _qk_inputs(q, k, q_weight, k_weight, cos, sin, positions, eps, style):
+    """Checks shared by the two forms: the C arguments up to the outputs."""
+    ldq, hsq = _heads(q, "q")
+    dev, (T, Hq, D) = q.device, q.shape
+    dt = _dtype_code(q)
+    ldk, hsk = _heads(k, "k", q.dtype, dev)
+    Hk = k.shape[1]
+    if k.shape[0] != T or k.shape[2] != D:
+        raise ValueError(f"k must have shape ({T}, heads, {D}) (got {tuple(k.shape)})")
+    w_dt = torch.float32
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            w_dt = w.dtype if isinstance(w, torch.Tensor) else None
+            _flat(w, name, D, dev, w_dt)
+            if w_dt not in _FLOATS:
+                raise ValueError(f"{name} must be bfloat16 or float32")
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise ValueError("q_weight and k_weight must have one dtype")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin must be given together")
+    ldt = rows = rot = 0
+    if cos is not None:
+        ldt = _matrix(cos, "cos", torch.float32, dev)
+        if _matrix(sin, "sin", torch.float32, dev, cos.shape) != ldt:
+            raise ValueError("cos and sin must have one row pitch")
+        rows, rot = cos.shape[0], 2 * cos.shape[1]
+    if positions is not None:
+        _flat(positions, "positions", T, dev, torch.int64)
+    if style not in ROPE_STYLES:
+        raise ValueError(f"style must be one of {sorted(ROPE_STYLES)}")
+    return (q.data_ptr(), Hq, ldq, hsq, k.data_ptr(), Hk, ldk, hsk, dt, T, D, _opt(q_weight), _opt(k_weight),
+            MXQ_BF16 if w_dt == torch.bfloat16 else MXQ_F32, eps, _opt(cos), _opt(sin), ldt, rows, rot,
+            _opt(positions), ROPE_STYLES[style])
+
+
+def _head_out(x, out, name, dtype):
+    if out is None:
+        out = torch.empty(x.shape, dtype=dtype, device=x.device)
+    return out, _heads(out, name, dtype, x.device, x.shape)
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions=None, eps=1e-6, style="interleaved", out_q=None,
+                 out_k=None):
+    """Root-mean-square norm of every query and key head, with the position rotation in the same pass.
+
+    ``q`` [T, Hq, D] and ``k`` [T, Hk, D], bf16 or fp32, views of a QKV projection's output as they are (heads
+    contiguous, D a multiple of 8 up to 512).  ``q_weight``, ``k_weight``: [D] or None.  ``cos``, ``sin``: float32
+    [P, R / 2], R <= D the rotated width, or None for the norm alone.  ``positions``: int64 [T], rows of the tables
+    (token t has row t if None); a position outside the tables gives NaN.  ``style``: the pairs that turn,
+    "interleaved" (2i, 2i+1) or "halves" (i, i + R/2).  Returns (q, k) of the input's type; ``out_q=q`` and
+    ``out_k=k`` work in place."""
+    args = _qk_inputs(q, k, q_weight, k_weight, cos, sin, positions, eps, style)
+    out_q, (ldq, hsq) = _head_out(q, out_q, "out_q", q.dtype)
+    out_k, (ldk, hsk) = _head_out(k, out_k, "out_k", q.dtype)
+    _call(lib.mxq_qk_norm_rope, q.device, *args, out_q.data_ptr(), ldq, hsq, out_k.data_ptr(), ldk, hsk)
+    return out_q, out_k
+
+
+def quantize_qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions=None, eps=1e-6, style="interleaved"):
+    """qk_norm_rope, then the 8-bit rule of quantize_int8 for each token and head: (q codes int8 [T, Hq, D],
+    q scales float32 [T, Hq], k codes, k scales).  With D % 16 == 0, ``gemm_w8a8(qc[:, h], qs[:, h], kc[:, h],
+    ks[:, h])`` is the 8-bit score product of head h."""
+    args = _qk_inputs(q, k, q_weight, k_weight, cos, sin, positions, eps, style)
+    outs = []
+    for x in (q, k):
+        T, H, D = x.shape
+        outs += [torch.empty((T, H, D), dtype=torch.int8, device=x.device),
+                 torch.empty((T, H), dtype=torch.float32, device=x.device)]
+    qc, qs, kc, ks = outs
+    D, Hq, Hk = q.shape[2], q.shape[1], k.shape[1]
+    _call(lib.mxq_quantize_qk_norm_rope, q.device, *args, qc.data_ptr(), Hq * D, D, qs.data_ptr(), Hq,
+          kc.data_ptr(), Hk * D, D, ks.data_ptr(), Hk)
+    return qc, qs, kc, ks

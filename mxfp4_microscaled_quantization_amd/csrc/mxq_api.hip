@@ -98,6 +98,131 @@ mxq_status check_operand(const char* fn, const char* name, const void* p, int64_
   return MXQ_OK;
 }
 
+// Checks of the 8-bit product that do not concern the activations.
+mxq_status check_w8(const char* fn, const int8_t* w, int64_t ld_w, const float* w_scales, int64_t inc_ws,
+                    const float* bias, int64_t M, int64_t N, int64_t K, const void* out, mxq_dtype out_dt,
+                    int64_t ld_out) {
+  const int ob = dtype_bytes(out_dt);
+  if (ob == 0) return fail(MXQ_ERR_UNSUPPORTED, "%s: unknown output dtype %d", fn, (int)out_dt);
+  if (M < 0 || N < 0 || K < 0)
+    return fail(MXQ_ERR_INVALID_ARG, "%s: negative size (M=%lld N=%lld K=%lld)", fn, (long long)M, (long long)N,
+                (long long)K);
+  if (K % 16 != 0) return fail(MXQ_ERR_INVALID_ARG, "%s: K (%lld) must be a multiple of 16", fn, (long long)K);
+  if (K >= ((int64_t)1 << 17))
+    return fail(MXQ_ERR_INVALID_ARG, "%s: K (%lld) must be below 2^17 (int32 sums)", fn, (long long)K);
+  if (M > kMaxDim - 256 || N > kMaxDim - 256) return fail(MXQ_ERR_INVALID_ARG, "%s: dimension too large", fn);
+  if (ld_out < N) return fail(MXQ_ERR_INVALID_ARG, "%s: ld_out (%lld) < N (%lld)", fn, (long long)ld_out, (long long)N);
+  if (!pitch_ok(ld_out)) return fail(MXQ_ERR_INVALID_ARG, "%s: ld_out (%lld) must be below 2^32", fn, (long long)ld_out);
+  if (ld_w < K || ld_w >= ((int64_t)1 << 23))
+    return fail(MXQ_ERR_INVALID_ARG, "%s: ld_w (%lld) must be at least K and below 2^23", fn, (long long)ld_w);
+  if (inc_ws < 0 || !pitch_ok(inc_ws)) return fail(MXQ_ERR_INVALID_ARG, "%s: inc_ws out of range", fn);
+  if (M > 0 && N > 0) {
+    if (((M + 255) / 256) * ((N + 255) / 256) > ((int64_t)1 << 22))   // threads of a launch stay below 2^32
+      return fail(MXQ_ERR_INVALID_ARG, "%s: problem too large", fn);
+    if (!out) return fail(MXQ_ERR_INVALID_ARG, "%s: out is NULL", fn);
+    if (!aligned(out, (uintptr_t)ob)) return fail(MXQ_ERR_INVALID_ARG, "%s: out must be %d-byte aligned", fn, ob);
+    if (!w_scales || !aligned(w_scales, 4))
+      return fail(MXQ_ERR_INVALID_ARG, "%s: w_scales must be a non-NULL 4-byte aligned pointer", fn);
+    if (!aligned(bias, 4)) return fail(MXQ_ERR_INVALID_ARG, "%s: bias must be 4-byte aligned", fn);
+    if (K > 0) {
+      if (!w) return fail(MXQ_ERR_INVALID_ARG, "%s: w is NULL", fn);
+      if (!aligned(w, 16) || ld_w % 16 != 0)
+        return fail(MXQ_ERR_INVALID_ARG, "%s: w base and ld_w must be multiples of 16 bytes", fn);
+    }
+  }
+  return MXQ_OK;
+}
+
+// Arguments of one side (queries or keys) of the head norm.
+struct HeadArgs {
+  const char* name;
+  const void* x;
+  int64_t heads, ld, hs;
+  const void* w;
+  void* out;
+  int64_t ld_o, hs_o;
+  float* scales;
+  int64_t ld_s;
+};
+
+mxq_status check_heads(const char* fn, const HeadArgs& h, int bytes, int out_bytes, int out_align, int w_bytes,
+                       int64_t tokens, int64_t head_dim, bool quant) {
+  if (h.heads < 0 || h.heads > 65536)
+    return fail(MXQ_ERR_INVALID_ARG, "%s: heads_%s (%lld) must be 0 to 65536", fn, h.name, (long long)h.heads);
+  if (h.heads == 0 || tokens == 0) return MXQ_OK;
+  if (h.ld < 0 || h.hs < 0 || h.ld_o < 0 || h.hs_o < 0 || !pitch_ok(h.ld) || !pitch_ok(h.hs) || !pitch_ok(h.ld_o) ||
+      !pitch_ok(h.hs_o))
+    return fail(MXQ_ERR_INVALID_ARG, "%s: pitches of %s must be 0 to 2^32 - 1", fn, h.name);
+  if (!h.x || !h.out) return fail(MXQ_ERR_INVALID_ARG, "%s: %s or its output is NULL", fn, h.name);
+  if (!aligned(h.x, 16) || h.ld * bytes % 16 != 0 || h.hs * bytes % 16 != 0)
+    return fail(MXQ_ERR_INVALID_ARG, "%s: %s base and pitches must be 16-byte aligned", fn, h.name);
+  if (!aligned(h.out, (uintptr_t)out_align) || h.ld_o * out_bytes % out_align != 0 || h.hs_o * out_bytes % out_align != 0)
+    return fail(MXQ_ERR_INVALID_ARG, "%s: output base and pitches of %s must be %d-byte aligned", fn, h.name, out_align);
+  // every (token, head) has a place of its own in the output
+  if ((h.heads > 1 && h.hs_o < head_dim) || (tokens > 1 && h.ld_o < head_dim))
+    return fail(MXQ_ERR_INVALID_ARG, "%s: output pitches of %s below head_dim", fn, h.name);
+  if (h.w && !aligned(h.w, (uintptr_t)(4 * w_bytes)))
+    return fail(MXQ_ERR_INVALID_ARG, "%s: w_%s must be %d-byte aligned", fn, h.name, 4 * w_bytes);
+  if (quant) {
+    if (!h.scales || !aligned(h.scales, 4))
+      return fail(MXQ_ERR_INVALID_ARG, "%s: scales_%s must be a non-NULL 4-byte aligned pointer", fn, h.name);
+    if (!pitch_ok(h.ld_s) || (tokens > 1 && h.ld_s < h.heads))
+      return fail(MXQ_ERR_INVALID_ARG, "%s: ld of scales_%s below its heads", fn, h.name);
+  }
+  return MXQ_OK;
+}
+
+mxq_status qk_norm_rope(const char* fn, HeadArgs q, HeadArgs k, mxq_dtype dt, int64_t tokens, int64_t head_dim,
+                        mxq_dtype w_dt, float eps, const float* cos, const float* sin, int64_t ld_table,
+                        int64_t table_rows, int64_t rot_dim, const int64_t* positions, mxq_rope_style style,
+                        bool quant, hipStream_t stream) {
+  const int bytes = dtype_bytes(dt), w_bytes = dtype_bytes(w_dt);
+  if (bytes == 0 || w_bytes == 0) return fail(MXQ_ERR_UNSUPPORTED, "%s: unknown dtype %d or %d", fn, (int)dt, (int)w_dt);
+  if (style != MXQ_ROPE_INTERLEAVED && style != MXQ_ROPE_HALVES)
+    return fail(MXQ_ERR_UNSUPPORTED, "%s: unknown rotation style %d", fn, (int)style);
+  if (tokens < 0 || tokens > kMaxDim) return fail(MXQ_ERR_INVALID_ARG, "%s: tokens (%lld) out of range", fn, (long long)tokens);
+  if (head_dim < 8 || head_dim > 512 || head_dim % 8 != 0)
+    return fail(MXQ_ERR_INVALID_ARG, "%s: head_dim (%lld) must be a multiple of 8, 8 to 512", fn, (long long)head_dim);
+  if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 8 != 0)
+    return fail(MXQ_ERR_INVALID_ARG, "%s: rot_dim (%lld) must be a multiple of 8, 0 to head_dim", fn, (long long)rot_dim);
+  if (!(eps >= 0.0f) || !(eps < __builtin_inff())) return fail(MXQ_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", fn);
+  const int out_bytes = quant ? 1 : bytes, out_align = quant ? 8 : 16;
+  for (const HeadArgs* h : {&q, &k}) {
+    const mxq_status st = check_heads(fn, *h, bytes, out_bytes, out_align, w_bytes, tokens, head_dim, quant);
+    if (st != MXQ_OK) return st;
+  }
+  if (tokens == 0 || q.heads + k.heads == 0) return ok();
+  if (rot_dim > 0) {
+    if (!cos || !sin || !aligned(cos, 16) || !aligned(sin, 16))
+      return fail(MXQ_ERR_INVALID_ARG, "%s: cos and sin must be non-NULL and 16-byte aligned", fn);
+    if (ld_table < rot_dim / 2 || ld_table % 4 != 0 || !pitch_ok(ld_table))
+      return fail(MXQ_ERR_INVALID_ARG, "%s: ld_table (%lld) must be a multiple of 4, at least rot_dim / 2", fn,
+                  (long long)ld_table);
+    if (table_rows < 0 || table_rows > kMaxDim || (!positions && table_rows < tokens))
+      return fail(MXQ_ERR_INVALID_ARG, "%s: table_rows (%lld) below the tokens without positions", fn,
+                  (long long)table_rows);
+    if (!aligned(positions, 8)) return fail(MXQ_ERR_INVALID_ARG, "%s: positions must be 8-byte aligned", fn);
+  }
+  auto side = [](const HeadArgs& h) {
+    return mxq::QkSide{h.x, h.heads > 0 ? h.w : nullptr, h.out, h.scales, h.ld, h.hs, h.ld_o, h.hs_o, h.ld_s, (int)h.heads};
+  };
+  mxq::QkNormParams p;
+  p.q = side(q);
+  p.k = side(k);
+  p.tokens = tokens;
+  p.ld_table = ld_table;
+  p.table_rows = table_rows;
+  p.cos = cos;
+  p.sin = sin;
+  p.positions = positions;
+  p.head_dim = (int)head_dim;
+  p.rot_dim = (int)rot_dim;
+  p.w_f32 = w_dt == MXQ_F32 ? 1 : 0;
+  p.eps = eps;
+  p.inv_dim = 1.0f / (float)head_dim;
+  return hip_status(fn, mxq::launch_qk_norm_rope(p, dt == MXQ_F32, quant, style == MXQ_ROPE_HALVES, stream));
+}
+
 hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 
 }  // namespace
@@ -407,6 +532,120 @@ mxq_status mxq_mfma_ceiling(mxq_gemm_mode mode, const void* a, const uint8_t* a_
   const mxq::GemmMode gm = mode == MXQ_GEMM_W4A4 ? mxq::GEMM_W4A4 : (mode == MXQ_GEMM_W4A8 ? mxq::GEMM_W4A8 : mxq::GEMM_BF16);
   return hip_status(fn, mxq::launch_mfma_ceiling(gm, a, a_scales, w, w_scales, M, N, K, waves, iters, sink,
                                                  as_stream(stream)));
+}
+
+mxq_status mxq_quantize_int8(const void* x, mxq_dtype dt, int64_t rows, int64_t cols, int64_t ld_x, int8_t* codes,
+                             int64_t ld_codes, float* scales, void* stream) {
+  const char* fn = "mxq_quantize_int8";
+  mxq_status st = check_input(fn, x, dt, rows, cols, ld_x, 16);
+  if (st != MXQ_OK) return st;
+  if (ld_codes < cols) return fail(MXQ_ERR_INVALID_ARG, "%s: ld_codes (%lld) < cols", fn, (long long)ld_codes);
+  if (!pitch_ok(ld_codes)) return fail(MXQ_ERR_INVALID_ARG, "%s: ld_codes (%lld) must be below 2^32", fn, (long long)ld_codes);
+  if (rows > 0 && cols > 0) {
+    if (!codes) return fail(MXQ_ERR_INVALID_ARG, "%s: codes is NULL", fn);
+    if (!aligned(codes, 16) || ld_codes % 16 != 0)
+      return fail(MXQ_ERR_INVALID_ARG, "%s: codes base and ld_codes must be multiples of 16 bytes", fn);
+  }
+  if (rows > 0 && (!scales || !aligned(scales, 4)))
+    return fail(MXQ_ERR_INVALID_ARG, "%s: scales must be a non-NULL 4-byte aligned pointer", fn);
+  return hip_status(fn, mxq::launch_quantize_int8(x, dt == MXQ_F32, rows, cols, ld_x, codes, ld_codes, scales,
+                                                  as_stream(stream)));
+}
+
+mxq_status mxq_dequantize_int8(const int8_t* codes, int64_t ld_codes, const float* scales, int64_t rows, int64_t cols,
+                               uint16_t* y, int64_t ld_y, void* stream) {
+  const char* fn = "mxq_dequantize_int8";
+  if (rows < 0 || cols < 0 || cols % 8 != 0)
+    return fail(MXQ_ERR_INVALID_ARG, "%s: cols must be a multiple of 8, sizes not negative", fn);
+  if (ld_codes < cols || ld_y < cols) return fail(MXQ_ERR_INVALID_ARG, "%s: pitch below the row width", fn);
+  if (rows > kMaxDim || cols > kMaxDim) return fail(MXQ_ERR_INVALID_ARG, "%s: dimension exceeds 2^31-1", fn);
+  if (!pitch_ok(ld_codes) || !pitch_ok(ld_y)) return fail(MXQ_ERR_INVALID_ARG, "%s: pitch must be below 2^32", fn);
+  if (rows * (cols / 8) >= ((int64_t)1 << 32))
+    return fail(MXQ_ERR_INVALID_ARG, "%s: tensor too large (more than 2^35 elements)", fn);
+  if (rows > 0 && cols > 0) {
+    if (!codes || !scales || !y) return fail(MXQ_ERR_INVALID_ARG, "%s: codes/scales/y is NULL", fn);
+    if (!aligned(codes, 8) || ld_codes % 8 != 0)
+      return fail(MXQ_ERR_INVALID_ARG, "%s: codes base and ld_codes must be multiples of 8 bytes", fn);
+    if (!aligned(scales, 4)) return fail(MXQ_ERR_INVALID_ARG, "%s: scales must be 4-byte aligned", fn);
+    if (!aligned(y, 16) || ld_y % 8 != 0)
+      return fail(MXQ_ERR_INVALID_ARG, "%s: y base and row pitch must be 16-byte aligned", fn);
+  }
+  return hip_status(fn, mxq::launch_dequantize_int8(codes, ld_codes, scales, rows, cols, y, ld_y, as_stream(stream)));
+}
+
+mxq_status mxq_gemm_w8a8(const int8_t* a, int64_t ld_a, const float* a_scales, int64_t inc_as, const int8_t* w,
+                         int64_t ld_w, const float* w_scales, int64_t inc_ws, const float* bias, int64_t M, int64_t N,
+                         int64_t K, void* out, mxq_dtype out_dt, int64_t ld_out, void* stream) {
+  const char* fn = "mxq_gemm_w8a8";
+  mxq_status st = check_w8(fn, w, ld_w, w_scales, inc_ws, bias, M, N, K, out, out_dt, ld_out);
+  if (st != MXQ_OK) return st;
+  if (ld_a < K || ld_a >= ((int64_t)1 << 23))
+    return fail(MXQ_ERR_INVALID_ARG, "%s: ld_a (%lld) must be at least K and below 2^23", fn, (long long)ld_a);
+  if (inc_as < 0 || !pitch_ok(inc_as)) return fail(MXQ_ERR_INVALID_ARG, "%s: inc_as out of range", fn);
+  if (M > 0 && N > 0) {
+    if (!a_scales || !aligned(a_scales, 4))
+      return fail(MXQ_ERR_INVALID_ARG, "%s: a_scales must be a non-NULL 4-byte aligned pointer", fn);
+    if (K > 0) {
+      if (!a) return fail(MXQ_ERR_INVALID_ARG, "%s: a is NULL", fn);
+      if (!aligned(a, 16) || ld_a % 16 != 0)
+        return fail(MXQ_ERR_INVALID_ARG, "%s: a base and ld_a must be multiples of 16 bytes", fn);
+    }
+  }
+  return hip_status(fn, mxq::launch_gemm_w8a8(a, ld_a, a_scales, inc_as, w, ld_w, w_scales, inc_ws, bias, M, N, K, out,
+                                              out_dt == MXQ_F32, ld_out, as_stream(stream)));
+}
+
+size_t mxq_gemm_w8a8_fused_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K < 0 || K % 16 != 0 || M > kMaxDim || K >= ((int64_t)1 << 17)) return 0;
+  return (size_t)M * (size_t)K + 4 * (size_t)M;   // codes, then scales
+}
+
+mxq_status mxq_gemm_w8a8_fused(const void* a, mxq_dtype dt, int64_t ld_a, const int8_t* w, int64_t ld_w,
+                               const float* w_scales, int64_t inc_ws, const float* bias, int64_t M, int64_t N,
+                               int64_t K, void* out, mxq_dtype out_dt, int64_t ld_out, void* workspace,
+                               size_t ws_bytes, void* stream) {
+  const char* fn = "mxq_gemm_w8a8_fused";
+  mxq_status st = check_w8(fn, w, ld_w, w_scales, inc_ws, bias, M, N, K, out, out_dt, ld_out);
+  if (st != MXQ_OK) return st;
+  st = check_input(fn, a, dt, M, K, ld_a, 16);
+  if (st != MXQ_OK) return st;
+  if (M == 0 || N == 0) return ok();
+  const size_t need = mxq_gemm_w8a8_fused_workspace_bytes(M, N, K);
+  if (need > 0 && (!workspace || !aligned(workspace, 16) || ws_bytes < need))
+    return fail(MXQ_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned and hold %llu bytes", fn,
+                (unsigned long long)need);
+  int8_t* codes = static_cast<int8_t*>(workspace);
+  float* scales = reinterpret_cast<float*>(codes + M * K);
+  hipError_t e = mxq::launch_quantize_int8(a, dt == MXQ_F32, M, K, ld_a, codes, K, scales, as_stream(stream));
+  if (e == hipSuccess)
+    e = mxq::launch_gemm_w8a8(codes, K, scales, 1, w, ld_w, w_scales, inc_ws, bias, M, N, K, out, out_dt == MXQ_F32,
+                              ld_out, as_stream(stream));
+  return hip_status(fn, e);
+}
+
+mxq_status mxq_qk_norm_rope(const void* q, int64_t heads_q, int64_t ld_q, int64_t hs_q, const void* k, int64_t heads_k,
+                            int64_t ld_k, int64_t hs_k, mxq_dtype dt, int64_t tokens, int64_t head_dim,
+                            const void* w_q, const void* w_k, mxq_dtype w_dt, float eps, const float* cos,
+                            const float* sin, int64_t ld_table, int64_t table_rows, int64_t rot_dim,
+                            const int64_t* positions, mxq_rope_style style, void* out_q, int64_t ld_oq, int64_t hs_oq,
+                            void* out_k, int64_t ld_ok, int64_t hs_ok, void* stream) {
+  return qk_norm_rope("mxq_qk_norm_rope", HeadArgs{"q", q, heads_q, ld_q, hs_q, w_q, out_q, ld_oq, hs_oq, nullptr, 0},
+                      HeadArgs{"k", k, heads_k, ld_k, hs_k, w_k, out_k, ld_ok, hs_ok, nullptr, 0}, dt, tokens, head_dim,
+                      w_dt, eps, cos, sin, ld_table, table_rows, rot_dim, positions, style, false, as_stream(stream));
+}
+
+mxq_status mxq_quantize_qk_norm_rope(const void* q, int64_t heads_q, int64_t ld_q, int64_t hs_q, const void* k,
+                                     int64_t heads_k, int64_t ld_k, int64_t hs_k, mxq_dtype dt, int64_t tokens,
+                                     int64_t head_dim, const void* w_q, const void* w_k, mxq_dtype w_dt, float eps,
+                                     const float* cos, const float* sin, int64_t ld_table, int64_t table_rows,
+                                     int64_t rot_dim, const int64_t* positions, mxq_rope_style style, int8_t* codes_q,
+                                     int64_t ld_cq, int64_t hs_cq, float* scales_q, int64_t ld_sq, int8_t* codes_k,
+                                     int64_t ld_ck, int64_t hs_ck, float* scales_k, int64_t ld_sk, void* stream) {
+  return qk_norm_rope("mxq_quantize_qk_norm_rope",
+                      HeadArgs{"q", q, heads_q, ld_q, hs_q, w_q, codes_q, ld_cq, hs_cq, scales_q, ld_sq},
+                      HeadArgs{"k", k, heads_k, ld_k, hs_k, w_k, codes_k, ld_ck, hs_ck, scales_k, ld_sk}, dt, tokens,
+                      head_dim, w_dt, eps, cos, sin, ld_table, table_rows, rot_dim, positions, style, true,
+                      as_stream(stream));
 }
 
 }  // extern "C"

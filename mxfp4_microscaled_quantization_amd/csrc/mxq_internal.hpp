@@ -41,6 +41,38 @@ hipError_t launch_mfma_ceiling(GemmMode mode, const void* a, const uint8_t* a_sc
                                const uint8_t* w_scales, int64_t M, int64_t N, int64_t K, int64_t waves, int64_t iters,
                                float* sink, hipStream_t stream);
 
+// 8-bit row quantization and dequantization (int8.hip).
+hipError_t launch_quantize_int8(const void* x, bool f32, int64_t rows, int64_t cols, int64_t ld_x, int8_t* codes,
+                                int64_t ld_codes, float* scales, hipStream_t stream);
+hipError_t launch_dequantize_int8(const int8_t* codes, int64_t ld_codes, const float* scales, int64_t rows,
+                                  int64_t cols, uint16_t* y, int64_t ld_y, hipStream_t stream);
+
+// 8-bit product with token and channel scales (gemm_int8.hip); inc_*: elements between
+// consecutive scales; bias may be null.
+hipError_t launch_gemm_w8a8(const int8_t* a, int64_t ld_a, const float* a_scales, int64_t inc_as, const int8_t* w,
+                            int64_t ld_w, const float* w_scales, int64_t inc_ws, const float* bias, int64_t M,
+                            int64_t N, int64_t K, void* out, bool f32_out, int64_t ld_out, hipStream_t stream);
+
+// Norm and rotation of query and key heads (qk_norm.hip).  Pitches in elements of the
+// tensor they belong to: ld_* between tokens, hs_* between heads.
+struct QkSide {
+  const void* x;
+  const void* w;      // head_dim weights, or null for 1
+  void* out;          // the input's type, or int8 codes
+  float* scales;      // of the codes
+  int64_t ld_x, hs_x, ld_o, hs_o, ld_s;
+  int heads;
+};
+struct QkNormParams {
+  QkSide q, k;
+  int64_t tokens, ld_table, table_rows;
+  const float *cos, *sin;
+  const int64_t* positions;   // or null: token t has position t
+  int head_dim, rot_dim, w_f32;
+  float eps, inv_dim;
+};
+hipError_t launch_qk_norm_rope(const QkNormParams& p, bool f32, bool quant, bool halves, hipStream_t stream);
+
 size_t sqnr_workspace_bytes(int64_t n);
 // The library's own SQNR workspace on the current device (a static device array,
 // sqnr_scratch_bytes() long): its device address, looked up once per device.

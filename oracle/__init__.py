@@ -20,6 +20,9 @@ exact integer / rational arithmetic) unless the method fixes a precision:
   per-element error budget |gpu - oracle| <= 1e-5 * sum|a*b| + 1 bf16 ulp.
 * ``sqnr``     -- whole-output signal-to-quantization-noise ratio in dB.
 * ``hadamard`` -- the fixed block-Hadamard rotation ahead of MXFP4, in binary32.
+* ``int8``     -- 8-bit row quantization and the 8-bit product with token and channel
+  scales.
+* ``qk_norm``  -- root-mean-square norm of query and key heads with the position rotation.
 
 Sources (web pages, cited by title and section):
 * "AMD Quark adds native W4A8 mixed-precision for Wan2.2 video generation on MI350",
@@ -43,7 +46,7 @@ Parity status: every public function is pinned by the ``-m "not gpu"`` tests aga
 closed forms, library routines, exact rational brute force or invariants.
 """
 
-from . import formats, mxfp4, fp8, gemm, sqnr, hadamard  # noqa: F401
+from . import formats, mxfp4, fp8, gemm, sqnr, hadamard, int8, qk_norm  # noqa: F401
 from .formats import (  # noqa: F401
     E2M1_MAGNITUDES, e2m1_decode, e8m0_decode, e4m3_decode, E4M3_MAX,
     bf16_bits_to_f64, f64_to_bf16_bits, bf16_ulp,
@@ -55,3 +58,5 @@ from .gemm import (  # noqa: F401
 )
 from .sqnr import sqnr_db  # noqa: F401
 from .hadamard import hadamard_matrix, rotate_f32, quantize_mxfp4_rotated  # noqa: F401
+from .int8 import quantize_int8, dequantize_int8, gemm_w8a8  # noqa: F401
+from .qk_norm import qk_norm_rope  # noqa: F401

@@ -1,0 +1,157 @@
+"""Norm and rotation of query and key heads on the GPU against the float64 oracle.
+
+Tolerance: the kernel's sum of squares has at most 15 roundings of non-negative terms, which
+the square root halves; the reciprocal root, x r, (x r) w, the two products and the sum of
+the rotation add at most 7 more, and the tables are exact inputs: 15 / 2 + 7 < 16 steps of
+2^-24, i.e. 2^-20 relative to |a c| + |b s|; then half a step of the output type."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from helpers import announce
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+HALF = {BF16: 2.0 ** -8, F32: 2.0 ** -24}
+
+
+def _inputs(T, Hq, Hk, D, R, P, dtype, wdtype, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    qkv = (torch.randn(T, (Hq + 2 * Hk) * D, generator=g) * scale).to(dtype).cuda()
+    q, k = qkv[:, :Hq * D].view(T, Hq, D), qkv[:, Hq * D:(Hq + Hk) * D].view(T, Hk, D)
+    wq, wk = ((1 + 0.3 * torch.randn(D, generator=g)).to(wdtype).cuda() for _ in range(2))
+    cos = sin = pos = None
+    if R:
+        ang = torch.rand(P, R // 2, generator=g, dtype=torch.float64) * 50
+        cos, sin = ang.cos().float().cuda(), ang.sin().float().cuda()
+        pos = torch.randint(0, P, (T,), generator=g).cuda()
+    return qkv, q, k, wq, wk, cos, sin, pos
+
+
+def _np(t):
+    return None if t is None else t.detach().double().cpu().numpy()
+
+
+def _oracle(x, w, cos, sin, pos, eps, style):
+    return oracle.qk_norm_rope(_np(x), _np(w), _np(cos), _np(sin), None if pos is None else pos.cpu().numpy(), eps, style)
+
+
+def _check(out, ref, size):
+    got = _np(out)
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+    tol = 2.0 ** -20 * size + HALF[out.dtype] * np.abs(ref) * (1 + 2.0 ** -12) + 2.0 ** -134
+    assert np.all((np.abs(got - ref) <= tol) | np.isnan(ref))
+
+
+CASES = [  # T, Hq, Hk, D, R
+    (1, 1, 1, 8, 8), (1, 32, 8, 128, 128), (2, 3, 1, 64, 64), (3, 5, 5, 72, 40), (7, 4, 2, 96, 64), (5, 24, 24, 128, 128),
+    (9, 2, 2, 256, 128), (4, 3, 2, 264, 264), (3, 2, 1, 512, 512), (33, 12, 3, 80, 40), (130, 40, 40, 128, 128),
+    (511, 2, 2, 64, 32), (512, 3, 2, 128, 64), (700, 5, 1, 80, 80), (515, 9, 7, 256, 256), (600, 2, 3, 512, 8), (513, 1, 0, 16, 16),
+    (513, 0, 4, 40, 24), (6, 0, 3, 128, 128), (6, 2, 0, 128, 0), (600, 17, 4, 64, 0), (520, 33, 33, 120, 56)]
+
+
+@pytest.mark.parametrize("style", ["interleaved", "halves"])
+@pytest.mark.parametrize("dtype,wdtype", [(BF16, BF16), (BF16, F32), (F32, F32), (F32, BF16)])
+@pytest.mark.parametrize("T,Hq,Hk,D,R", CASES)
+def test_matches_oracle(gpu, T, Hq, Hk, D, R, dtype, wdtype, style):
+    announce(f"qk_norm_rope T={T} {Hq}+{Hk}x{D} R={R} {dtype} w {wdtype} {style}")
+    qkv, q, k, wq, wk, cos, sin, pos = _inputs(T, Hq, Hk, D, R, 37, dtype, wdtype, T + D)
+    before = qkv.clone()
+    oq, ok = gpu.qk_norm_rope(q, k, wq, wk, cos, sin, positions=pos, eps=1e-5, style=style)
+    assert torch.equal(qkv, before)
+    _check(oq, *_oracle(q, wq, cos, sin, pos, 1e-5, style))
+    _check(ok, *_oracle(k, wk, cos, sin, pos, 1e-5, style))
+    # quantized: every value within half a step of its code, the step within its roundings
+    qc, qs, kc, ks = gpu.quantize_qk_norm_rope(q, k, wq, wk, cos, sin, positions=pos, eps=1e-5, style=style)
+    for c, s, x, w in ((qc, qs, q, wq), (kc, ks, k, wk)):
+        ref, size = _oracle(x, w, cos, sin, pos, 1e-5, style)
+        if ref.size == 0:
+            assert c.numel() == 0
+            continue
+        step = np.abs(ref).max(-1) / 127
+        off = 2.0 ** -20 * size.max(-1) / 127 + 2.0 ** -24 * step
+        assert np.all(np.abs(_np(s) - step) <= off)
+        # x inv: 127 steps times (2^-20 |size| / amax + two roundings), size <= sqrt(2) amax of the pair's
+        # length, itself at most sqrt(2) amax: below 127 * 2^-18
+        err = np.abs(_np(c) * _np(s)[..., None] - ref)
+        assert np.all(err <= (0.5 + 127 * 2.0 ** -18) * _np(s)[..., None] + 2.0 ** -20 * size)
+        assert np.abs(_np(c)).max() == 127
+
+
+def test_in_place_and_strided_heads(gpu):
+    """Outputs over the inputs; heads that are not next to each other ([T, H, 3, D] packing);
+    what lies between them stays."""
+    announce("qk_norm_rope in place")
+    T, H, D = 530, 3, 96
+    for dtype in (BF16, F32):
+        for style in ("interleaved", "halves"):
+            g = torch.Generator().manual_seed(2)
+            packed = torch.randn(T, H, 3, D, generator=g).to(dtype).cuda()
+            before = packed.clone()
+            q, k = packed[:, :, 0], packed[:, :, 1]
+            ang = torch.rand(T, D // 2, generator=g) * 9
+            cos, sin = ang.cos().cuda(), ang.sin().cuda()
+            rq, rk = gpu.qk_norm_rope(q, k, None, None, cos, sin, style=style)
+            _check(rq, *_oracle(q, None, cos, sin, None, 1e-6, style))
+            oq, ok = gpu.qk_norm_rope(q, k, None, None, cos, sin, style=style, out_q=q, out_k=k)
+            assert torch.equal(oq, rq) and torch.equal(ok, rk) and torch.equal(packed[:, :, 2], before[:, :, 2])
+
+
+def test_no_rotation_is_the_norm_alone(gpu):
+    announce("qk_norm_rope without tables")
+    _, q, k, wq, wk, _, _, _ = _inputs(12, 4, 2, 128, 0, 1, BF16, BF16, 7)
+    oq, ok = gpu.qk_norm_rope(q, k, wq, wk, None, None)
+    _check(oq, *_oracle(q, wq, None, None, None, 1e-6, "halves"))
+    _check(ok, *_oracle(k, wk, None, None, None, 1e-6, "halves"))
+
+
+@pytest.mark.parametrize("T", [4, 600])
+def test_positions_outside_the_table_give_nan(gpu, T):
+    announce(f"qk_norm_rope bad positions T={T}")
+    _, q, k, wq, wk, cos, sin, pos = _inputs(T, 2, 2, 96, 64, 10, BF16, BF16, 3)
+    pos[1], pos[2], pos[3] = -1, 10, 2 ** 62
+    good = pos.clone()
+    good[1:4] = 0
+    for style in ("interleaved", "halves"):
+        oq, ok = gpu.qk_norm_rope(q, k, wq, wk, cos, sin, positions=pos, style=style)
+        _check(oq, *_oracle(q, wq, cos, sin, pos, 1e-6, style))
+        assert oq[1:4, :, :64].isnan().all() and not oq[1:4, :, 64:].isnan().any() and not ok[4:].isnan().any()
+        rq, rk = gpu.qk_norm_rope(q, k, wq, wk, cos, sin, positions=good, style=style)
+        assert torch.equal(oq[4:], rq[4:]) and torch.equal(ok[0], rk[0])
+        qc, qs, kc, ks = gpu.quantize_qk_norm_rope(q, k, wq, wk, cos, sin, positions=pos, style=style)
+        assert qs[1:4].isnan().all() and not qc[1:4].any() and not qs[4:].isnan().any() and not ks[0].isnan().any()
+
+
+def test_degenerate_heads(gpu):
+    """Zero heads give zeros (eps > 0); an infinity or NaN stays in its head; large and small values."""
+    announce("qk_norm_rope degenerate heads")
+    _, q, k, wq, wk, cos, sin, pos = _inputs(8, 3, 3, 128, 128, 20, F32, F32, 5)
+    q = q.clone()
+    q[0, 1] = 0
+    q[1, 0, 5] = float("inf")
+    q[2, 2, 7] = float("nan")
+    q[3] *= 1e15
+    q[4] *= 1e-15
+    with np.errstate(all="ignore"):
+        ref, size = _oracle(q, wq, cos, sin, pos, 1e-6, "halves")
+    oq, _ = gpu.qk_norm_rope(q, k, wq, wk, cos, sin, positions=pos, style="halves")
+    assert (oq[0, 1] == 0).all()
+    keep = torch.ones(8, 3, dtype=torch.bool)
+    keep[1, 0] = keep[2, 2] = False
+    _check(oq.cpu()[keep], ref[keep.numpy()], size[keep.numpy()])
+    qc, qs, _, _ = gpu.quantize_qk_norm_rope(q, k, wq, wk, cos, sin, positions=pos, style="halves")
+    assert qs[0, 1] == 0 and not qc[0, 1].any() and qs[1, 0].isnan() and not qc[1, 0].any() and qs[2, 2].isnan()
+    assert int(qs.isnan().sum()) == 2
+
+
+def test_empty(gpu):
+    announce("qk_norm_rope empty")
+    e = torch.empty(0, 3, 64, device="cuda")
+    oq, ok = gpu.qk_norm_rope(e, e, None, None, None, None)
+    assert oq.shape == ok.shape == (0, 3, 64)
+    e = torch.empty(5, 0, 64, device="cuda")
+    qc, qs, kc, ks = gpu.quantize_qk_norm_rope(e, e, None, None, None, None)
+    assert qc.shape == (5, 0, 64) and ks.shape == (5, 0)
