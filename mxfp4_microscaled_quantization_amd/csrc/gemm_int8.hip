@@ -296,6 +296,80 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(I8Params p) {
   }
 }
 
+// ---------------------------------------------------------------------------------
+// A few tokens: the weights' bytes are what counts, each used by one workgroup only, so
+// they go from memory to registers.  One workgroup = 16 NI channels x 16 MJ tokens, its
+// WAVES waves splitting K (window w to wave w mod WAVES) with U windows of loads in flight
+// each; the partial sums meet in LDS (integers: the order changes nothing).
+template <int NI, int MJ, int WAVES, int U, bool F32OUT>
+__global__ __launch_bounds__(64 * WAVES) void gemm_i8_few_kernel(I8Params p) {
+  __shared__ __attribute__((aligned(16))) v4i part[WAVES][NI][MJ][64];
+  const uint32_t tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(tid >> 6));
+  const int n0 = (int)(blockIdx.x % (unsigned)p.tiles_n) * (16 * NI), m0 = (int)(blockIdx.x / (unsigned)p.tiles_n) * (16 * MJ);
+  const uint32_t rows_a = (uint32_t)min(16 * MJ, p.M - m0), rows_w = (uint32_t)min(16 * NI, p.N - n0);
+  const bool any = p.nwin > 0;
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a + (int64_t)m0 * p.ld_a, any ? (rows_a - 1) * p.ld_a + (uint32_t)p.K : 0u);
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.w + (int64_t)n0 * p.ld_w, any ? (rows_w - 1) * p.ld_w + (uint32_t)p.K : 0u);
+  v4i acc[NI][MJ];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < MJ; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+
+  for (int w0 = wave; w0 < p.nwin; w0 += WAVES * U) {
+    v4i fw[U][2][NI], fa[U][2][MJ];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        // lane group g takes chunk g of each 64-byte half window; past K both operands read
+        // from outside their resource, i.e. zeros
+        const uint32_t k = (uint32_t)(w0 + u * WAVES) * kWin + 64u * t + 16u * g;
+        const bool in = k < (uint32_t)p.K;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+          fw[u][t][i] = __builtin_bit_cast(
+              v4i, __builtin_amdgcn_raw_buffer_load_b128(rw, in ? (16 * i + r16) * p.ld_w + k : kOutside, 0, 0));
+#pragma unroll
+        for (int j = 0; j < MJ; ++j)
+          fa[u][t][j] = __builtin_bit_cast(
+              v4i, __builtin_amdgcn_raw_buffer_load_b128(ra, in ? (16 * j + r16) * p.ld_a + k : kOutside, 0, 0));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int j = 0; j < MJ; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][t][i], fa[u][t][j], acc[i][j], 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < MJ; ++j) part[wave][i][j][lane] = acc[i][j];
+  __syncthreads();
+  // thread e takes output (token e / (16 NI), channel e % (16 NI)) of the tile
+  const bool has_bias = p.bias != nullptr;
+  for (uint32_t e = tid; e < 16 * NI * rows_a; e += 64 * WAVES) {
+    const uint32_t m = e / (16 * NI), n = e % (16 * NI);
+    if (n >= rows_w) continue;
+    const uint32_t from = ((n & 15) >> 2) * 16 + (m & 15);
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) sum += reinterpret_cast<const int*>(&part[w][n >> 4][m >> 4][from])[n & 3];
+    const int64_t mm = m0 + (int)m, nn = n0 + (int)n;
+    const float v = scaled(sum, p.a_scales[mm * p.inc_as], p.w_scales[nn * p.inc_ws], has_bias ? p.bias[nn] : 0.0f, has_bias);
+    if constexpr (F32OUT)
+      static_cast<float*>(p.out)[mm * p.ld_out + nn] = v;
+    else
+      static_cast<uint16_t*>(p.out)[mm * p.ld_out + nn] = (uint16_t)pack_bf16x2(v, 0.0f);
+  }
+}
+
 }  // namespace
 
 hipError_t launch_gemm_w8a8(const int8_t* a, int64_t ld_a, const float* a_scales, int64_t inc_as, const int8_t* w,
@@ -324,10 +398,18 @@ hipError_t launch_gemm_w8a8(const int8_t* a, int64_t ld_a, const float* a_scales
     p.tiles_n = (int)((N + bn - 1) / bn);
     hipLaunchKernelGGL(kernel, dim3((unsigned)(p.tiles_m * p.tiles_n)), dim3(64 * waves), 0, stream, p);
   };
-  if (f32_out)
-    tile(gemm_i8_kernel<4, 8, 2, 4, 3, 2, true>, 256, 256, 8);
-  else
-    tile(gemm_i8_kernel<4, 8, 2, 4, 3, 2, false>, 256, 256, 8);
+  auto pick = [&](auto f_tag) {
+    constexpr bool F = decltype(f_tag)::value;
+    if (M <= 16)
+      tile(gemm_i8_few_kernel<1, 1, 8, 4, F>, 16, 16, 8);
+    else if (M <= 32)
+      tile(gemm_i8_few_kernel<1, 2, 8, 4, F>, 32, 16, 8);
+    else if (M <= 64)
+      tile(gemm_i8_few_kernel<2, 4, 8, 2, F>, 64, 32, 8);
+    else
+      tile(gemm_i8_kernel<4, 8, 2, 4, 3, 2, F>, 256, 256, 8);
+  };
+  f32_out ? pick(std::true_type{}) : pick(std::false_type{});
   return hipGetLastError();
 }
 
