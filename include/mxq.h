@@ -344,11 +344,23 @@ mxq_status mxq_dequantize_int8(const int8_t* codes, int64_t ld_codes, const floa
  *     one scale for all).  bias : float[N] or NULL.
  * out : M x N of out_dt, pitch ld_out elements (>= N), naturally aligned.
  * K % 16 == 0 and K < 2^17 (the sum then fits int32); K == 0 gives the bias, or zeros.
+ * workspace, ws_bytes : NULL (0), or device memory of at least
+ *     mxq_gemm_w8a8_workspace_bytes(M, N, K) bytes, 16-byte aligned, owned by the caller and
+ *     not used by anything else until the call's work on `stream` is done.  With one, a
+ *     long K over few output tiles is split over the GPU and summed in a second launch;
+ *     the bits are the same either way.
  */
 mxq_status mxq_gemm_w8a8(const int8_t* a, int64_t ld_a, const float* a_scales, int64_t inc_as,
                          const int8_t* w, int64_t ld_w, const float* w_scales, int64_t inc_ws,
                          const float* bias, int64_t M, int64_t N, int64_t K, void* out,
-                         mxq_dtype out_dt, int64_t ld_out, void* stream);
+                         mxq_dtype out_dt, int64_t ld_out, void* workspace, size_t ws_bytes,
+                         void* stream);
+
+/*
+ * mxq_gemm_w8a8_workspace_bytes -- workspace with which mxq_gemm_w8a8 splits K for a shape: 0
+ * where it does not (or for an empty or invalid shape).  Host only; no device work.
+ */
+size_t mxq_gemm_w8a8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /*
  * mxq_gemm_w8a8_fused -- mxq_gemm_w8a8 on unquantized activations, equal bit for bit to

@@ -21,7 +21,8 @@ import torch
 __all__ = [
     "lib", "MxqError", "quantize", "quantize_into", "quantize_hadamard", "SCALE_RULES", "quantize_fp8", "absmax", "fp8_static_scales",
     "gemm_w4a4", "gemm_w4a4_fused", "gemm_w4a8", "gemm_bf16", "sqnr", "sqnr_noalloc", "sqnr_workspace_bytes", "dequantize", "dequantize_fp8",
-    "quantize_int8", "dequantize_int8", "gemm_w8a8", "gemm_w8a8_fused", "w8a8_fused_workspace_bytes",
+    "quantize_int8", "dequantize_int8", "gemm_w8a8", "gemm_w8a8_fused", "w8a8_workspace_bytes",
+    "w8a8_fused_workspace_bytes",
     "qk_norm_rope", "quantize_qk_norm_rope", "ROPE_STYLES", "mfma_ceiling", "MFMA_FLOP", "check_buffer",
     "LIB_PATH", "ABI_SYMBOLS", "ABI_VERSION",
 ]
@@ -66,7 +67,8 @@ ABI_SYMBOLS = {
     "mxq_quantize_int8": (ctypes.c_int, [_ptr, ctypes.c_int, _i64, _i64, _i64, _ptr, _i64, _ptr, _ptr]),
     "mxq_dequantize_int8": (ctypes.c_int, [_ptr, _i64, _ptr, _i64, _i64, _ptr, _i64, _ptr]),
     "mxq_gemm_w8a8": (ctypes.c_int, [_ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _i64, _i64, _ptr,
-                                     ctypes.c_int, _i64, _ptr]),
+                                     ctypes.c_int, _i64, _ptr, _sz, _ptr]),
+    "mxq_gemm_w8a8_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "mxq_gemm_w8a8_fused": (ctypes.c_int, [_ptr, ctypes.c_int, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _i64, _i64,
                                            _ptr, ctypes.c_int, _i64, _ptr, _sz, _ptr]),
     "mxq_gemm_w8a8_fused_workspace_bytes": (_sz, [_i64, _i64, _i64]),
@@ -554,9 +556,16 @@ def gemm_w8a8(a_codes, a_scales, w_codes, w_scales, bias=None, out=None, out_dty
     if bias is not None:
         _flat(bias, "bias", N, dev)
     out, ld = _w8_out(M, N, dev, out, out_dtype)
+    nbytes = lib.mxq_gemm_w8a8_workspace_bytes(M, N, K)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     _call(lib.mxq_gemm_w8a8, dev, a_codes.data_ptr(), lda, a_scales.data_ptr(), inc_a, w_codes.data_ptr(), ldw,
-          w_scales.data_ptr(), inc_w, _opt(bias), M, N, K, out.data_ptr(), _dtype_code(out), ld)
+          w_scales.data_ptr(), inc_w, _opt(bias), M, N, K, out.data_ptr(), _dtype_code(out), ld, _opt(ws), nbytes)
     return out
+
+
+def w8a8_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Workspace bytes with which gemm_w8a8 splits K for a shape (0 where it does not)."""
+    return int(lib.mxq_gemm_w8a8_workspace_bytes(M, N, K))
 
 
 def w8a8_fused_workspace_bytes(M: int, N: int, K: int) -> int:

@@ -133,6 +133,14 @@ mxq_status check_w8(const char* fn, const int8_t* w, int64_t ld_w, const float* 
   return MXQ_OK;
 }
 
+// Shapes for which the 8-bit workspaces have a size.
+bool w8_shape_ok(int64_t M, int64_t N, int64_t K) {
+  return M > 0 && N > 0 && K >= 0 && K % 16 == 0 && M <= kMaxDim - 256 && N <= kMaxDim - 256 && K < ((int64_t)1 << 17);
+}
+
+// Codes and scales of quantized activations, in 16-byte steps.
+size_t fused_codes_bytes(int64_t M, int64_t K) { return (size_t)M * (size_t)K + ((size_t)M + 3) / 4 * 16; }
+
 // Arguments of one side (queries or keys) of the head norm.
 struct HeadArgs {
   const char* name;
@@ -573,9 +581,15 @@ mxq_status mxq_dequantize_int8(const int8_t* codes, int64_t ld_codes, const floa
   return hip_status(fn, mxq::launch_dequantize_int8(codes, ld_codes, scales, rows, cols, y, ld_y, as_stream(stream)));
 }
 
+size_t mxq_gemm_w8a8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (!w8_shape_ok(M, N, K)) return 0;
+  return mxq::gemm_w8a8_workspace_bytes(M, N, K);
+}
+
 mxq_status mxq_gemm_w8a8(const int8_t* a, int64_t ld_a, const float* a_scales, int64_t inc_as, const int8_t* w,
                          int64_t ld_w, const float* w_scales, int64_t inc_ws, const float* bias, int64_t M, int64_t N,
-                         int64_t K, void* out, mxq_dtype out_dt, int64_t ld_out, void* stream) {
+                         int64_t K, void* out, mxq_dtype out_dt, int64_t ld_out, void* workspace, size_t ws_bytes,
+                         void* stream) {
   const char* fn = "mxq_gemm_w8a8";
   mxq_status st = check_w8(fn, w, ld_w, w_scales, inc_ws, bias, M, N, K, out, out_dt, ld_out);
   if (st != MXQ_OK) return st;
@@ -590,14 +604,17 @@ mxq_status mxq_gemm_w8a8(const int8_t* a, int64_t ld_a, const float* a_scales, i
       if (!aligned(a, 16) || ld_a % 16 != 0)
         return fail(MXQ_ERR_INVALID_ARG, "%s: a base and ld_a must be multiples of 16 bytes", fn);
     }
+    if (workspace && (!aligned(workspace, 16) || ws_bytes < mxq_gemm_w8a8_workspace_bytes(M, N, K)))
+      return fail(MXQ_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned and hold %llu bytes", fn,
+                  (unsigned long long)mxq_gemm_w8a8_workspace_bytes(M, N, K));
   }
   return hip_status(fn, mxq::launch_gemm_w8a8(a, ld_a, a_scales, inc_as, w, ld_w, w_scales, inc_ws, bias, M, N, K, out,
-                                              out_dt == MXQ_F32, ld_out, as_stream(stream)));
+                                              out_dt == MXQ_F32, ld_out, workspace, as_stream(stream)));
 }
 
 size_t mxq_gemm_w8a8_fused_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (M <= 0 || N <= 0 || K < 0 || K % 16 != 0 || M > kMaxDim || K >= ((int64_t)1 << 17)) return 0;
-  return (size_t)M * (size_t)K + 4 * (size_t)M;   // codes, then scales
+  if (!w8_shape_ok(M, N, K)) return 0;
+  return fused_codes_bytes(M, K) + mxq::gemm_w8a8_workspace_bytes(M, N, K);
 }
 
 mxq_status mxq_gemm_w8a8_fused(const void* a, mxq_dtype dt, int64_t ld_a, const int8_t* w, int64_t ld_w,
@@ -616,10 +633,11 @@ mxq_status mxq_gemm_w8a8_fused(const void* a, mxq_dtype dt, int64_t ld_a, const 
                 (unsigned long long)need);
   int8_t* codes = static_cast<int8_t*>(workspace);
   float* scales = reinterpret_cast<float*>(codes + M * K);
+  void* rest = mxq::gemm_w8a8_workspace_bytes(M, N, K) > 0 ? codes + fused_codes_bytes(M, K) : nullptr;
   hipError_t e = mxq::launch_quantize_int8(a, dt == MXQ_F32, M, K, ld_a, codes, K, scales, as_stream(stream));
   if (e == hipSuccess)
     e = mxq::launch_gemm_w8a8(codes, K, scales, 1, w, ld_w, w_scales, inc_ws, bias, M, N, K, out, out_dt == MXQ_F32,
-                              ld_out, as_stream(stream));
+                              ld_out, rest, as_stream(stream));
   return hip_status(fn, e);
 }
 

@@ -48,10 +48,13 @@ hipError_t launch_dequantize_int8(const int8_t* codes, int64_t ld_codes, const f
                                   int64_t cols, uint16_t* y, int64_t ld_y, hipStream_t stream);
 
 // 8-bit product with token and channel scales (gemm_int8.hip); inc_*: elements between
-// consecutive scales; bias may be null.
+// consecutive scales; bias may be null.  workspace: gemm_w8a8_workspace_bytes, or null (K is
+// then not split; the same bits).
+size_t gemm_w8a8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_w8a8(const int8_t* a, int64_t ld_a, const float* a_scales, int64_t inc_as, const int8_t* w,
                             int64_t ld_w, const float* w_scales, int64_t inc_ws, const float* bias, int64_t M,
-                            int64_t N, int64_t K, void* out, bool f32_out, int64_t ld_out, hipStream_t stream);
+                            int64_t N, int64_t K, void* out, bool f32_out, int64_t ld_out, void* workspace,
+                            hipStream_t stream);
 
 // Norm and rotation of query and key heads (qk_norm.hip).  Pitches in elements of the
 // tensor they belong to: ld_* between tokens, hs_* between heads.

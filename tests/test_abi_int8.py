@@ -24,8 +24,9 @@ def _dequant(codes=OK16, ldc=64, scales=OK16, rows=4, cols=64, y=OK16, ldy=64):
     return mxq.lib.mxq_dequantize_int8(codes, ldc, scales, rows, cols, y, ldy, None)
 
 
-def _gemm(a=OK16, lda=64, sa=OK16, ia=1, w=OK16, ldw=64, sw=OK16, iw=1, bias=None, M=8, N=8, K=64, out=OK16, dt=1, ldo=8):
-    return mxq.lib.mxq_gemm_w8a8(a, lda, sa, ia, w, ldw, sw, iw, bias, M, N, K, out, dt, ldo, None)
+def _gemm(a=OK16, lda=64, sa=OK16, ia=1, w=OK16, ldw=64, sw=OK16, iw=1, bias=None, M=8, N=8, K=64, out=OK16, dt=1, ldo=8,
+          ws=None, nbytes=0):
+    return mxq.lib.mxq_gemm_w8a8(a, lda, sa, ia, w, ldw, sw, iw, bias, M, N, K, out, dt, ldo, ws, nbytes, None)
 
 
 def _fused(a=OK16, dt=1, lda=64, w=OK16, ldw=64, sw=OK16, iw=1, bias=None, M=8, N=8, K=64, out=OK16, odt=1, ldo=8,
@@ -67,6 +68,8 @@ INVALID = [
     (_gemm, dict(bias=ODD2), "bias"), (_gemm, dict(out=None), "out is NULL"), (_gemm, dict(out=P(0x10001)), "2-byte"),
     (_gemm, dict(out=ODD2, dt=0), "4-byte"), (_gemm, dict(ldo=7), "ld_out"), (_gemm, dict(ldo=BIG), "ld_out"),
     (_gemm, dict(M=2 ** 30, N=2 ** 20, ldo=2 ** 20), "too large"),
+    (_gemm, dict(ws=ODD8, nbytes=1 << 30), "workspace"),
+    (_gemm, dict(M=48, N=5120, K=13824, lda=13824, ldw=13824, ldo=5120, ws=OK16, nbytes=16), "workspace"),
     (_fused, dict(K=56, lda=56), "multiple of 16"), (_fused, dict(lda=48), "ld_x"), (_fused, dict(lda=68), "aligned"),
     (_fused, dict(a=ODD8), "aligned"), (_fused, dict(a=None), "NULL"), (_fused, dict(w=None), "w is NULL"),
     (_fused, dict(M=64, ws=None), "workspace"), (_fused, dict(M=64, ws=ODD8), "workspace"),
@@ -115,7 +118,9 @@ def test_workspace_covers_codes_and_scales():
     for M, N, K in ((300, 64, 128), (4096, 5120, 13824)):
         assert mxq.w8a8_fused_workspace_bytes(M, N, K) >= M * K + 4 * M
     for M, N, K in ((0, 8, 64), (8, 0, 64), (8, 8, 40), (-1, 8, 64), (8, 8, 1 << 17), (8, 8, -16)):
-        assert mxq.w8a8_fused_workspace_bytes(M, N, K) == 0
+        assert mxq.w8a8_fused_workspace_bytes(M, N, K) == 0 and mxq.w8a8_workspace_bytes(M, N, K) == 0
+    assert mxq.w8a8_workspace_bytes(48, 5120, 13824) > 0 and mxq.w8a8_workspace_bytes(4096, 5120, 13824) == 0
+    assert mxq.w8a8_fused_workspace_bytes(48, 5120, 13824) >= 48 * 13828 + mxq.w8a8_workspace_bytes(48, 5120, 13824)
 
 
 # ------------------------------------------------------------------ binding

@@ -166,7 +166,11 @@ SHAPES = [(1, 1, 16), (1, 5120, 1360), (2, 3, 131056), (1, 17, 4096), (3, 16, 64
           (16, 256, 2048), (17, 255, 272), (31, 64, 112), (32, 48, 4112), (33, 1000, 240), (48, 640, 1024), (63, 129, 80),
           (64, 512, 13824), (65, 257, 384), (100, 320, 96), (127, 130, 528), (128, 128, 256), (129, 1, 1040),
           (200, 640, 640), (255, 300, 48), (256, 256, 512), (257, 511, 1360), (300, 2051, 160), (513, 769, 2064),
-          (1001, 2051, 1360), (2048, 96, 320), (1, 13824, 5120), (5, 40000, 32)]
+          (1001, 2051, 1360), (2048, 96, 320), (1, 13824, 5120), (5, 40000, 32),
+          # every tile, and splits of K with a ragged last part
+          (9, 5120, 96), (30, 13824, 160), (48, 5120, 13824), (60, 515, 13808), (60, 7000, 304), (130, 5120, 1040), (250, 13824, 272),
+          (256, 5120, 8192), (500, 5120, 400), (500, 770, 16000), (700, 13824, 144), (1300, 5120, 272), (2100, 5000, 160),
+          (64, 256, 131056)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
