@@ -453,13 +453,20 @@ def dequantize_fp8(q, a_scale: float, out=None) -> torch.Tensor:
 # ---------------------------------------------------------------------------------
 # 8-bit integers.  These entry points launch on the tensors' own device, whichever is current.
 
+# the raw stream handle without building a Stream object (2 us of the 10 us of a small call); None without a GPU build
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _call(fn, device, *args):
     """``fn(*args, stream)`` with torch's current stream of ``device``, checked."""
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)))
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)))
+            status = fn(*args, _raw_stream(index))
+    if status != MXQ_OK:
+        _check(status)
 
 
 def _matrix(t, name, dtype, device=None, shape=None):
@@ -469,12 +476,13 @@ def _matrix(t, name, dtype, device=None, shape=None):
         raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    pitch, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.stride(0) if rows > 1 else cols
+    return pitch if rows > 1 else cols
 
 
 def _vector(t, name, n, device, dtype=torch.float32):
@@ -482,7 +490,7 @@ def _vector(t, name, n, device, dtype=torch.float32):
     _dev(t, name, device)
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
-    if t.dim() != 1 or t.shape[0] != n:
+    if t.shape != (n,):
         raise ValueError(f"{name} must have shape ({n},) (got {tuple(t.shape)})")
     return t.stride(0) if n > 1 else 1
 
@@ -604,13 +612,15 @@ def _heads(t, name, dtype=None, device=None, shape=None):
         raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
     if t.dim() != 3:
         raise ValueError(f"{name} must be 3-D [tokens, heads, head_dim]")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
     T, H, D = t.shape
-    if D > 1 and t.stride(2) != 1:
+    ld, hs, step = t.stride()
+    if D > 1 and step != 1:
         raise ValueError(f"{name} must have contiguous heads")
-    hs = t.stride(1) if H > 1 else D
-    return (t.stride(0) if T > 1 else H * hs), hs
+    if H <= 1:
+        hs = D
+    return (ld if T > 1 else H * hs), hs
 
 
 def _qk_inputs(q, k, q_weight, k_weight, cos, sin, positions, eps, style):
@@ -619,39 +629,43 @@ def _qk_inputs(q, k, q_weight, k_weight, cos, sin, positions, eps, style):
     dev, (T, Hq, D) = q.device, q.shape
     dt = _dtype_code(q)
     ldk, hsk = _heads(k, "k", q.dtype, dev)
-    Hk = k.shape[1]
-    if k.shape[0] != T or k.shape[2] != D:
+    Tk, Hk, Dk = k.shape
+    if Tk != T or Dk != D:
         raise ValueError(f"k must have shape ({T}, heads, {D}) (got {tuple(k.shape)})")
-    w_dt = torch.float32
+    w_dt = None
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
-            w_dt = w.dtype if isinstance(w, torch.Tensor) else None
-            _flat(w, name, D, dev, w_dt)
-            if w_dt not in _FLOATS:
+            _dev(w, name, dev)
+            dtype = w.dtype
+            if dtype not in _FLOATS:
                 raise ValueError(f"{name} must be bfloat16 or float32")
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-        raise ValueError("q_weight and k_weight must have one dtype")
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin must be given together")
+            if w.shape != (D,) or w.stride(0) != 1:
+                raise ValueError(f"{name} must be contiguous, of shape ({D},) (got {tuple(w.shape)})")
+            if w_dt is not None and dtype != w_dt:
+                raise ValueError("q_weight and k_weight must have one dtype")
+            w_dt = dtype
     ldt = rows = rot = 0
-    if cos is not None:
+    if cos is not None and sin is not None:
         ldt = _matrix(cos, "cos", torch.float32, dev)
         if _matrix(sin, "sin", torch.float32, dev, cos.shape) != ldt:
             raise ValueError("cos and sin must have one row pitch")
-        rows, rot = cos.shape[0], 2 * cos.shape[1]
+        rows, rot = cos.shape
+    elif cos is not None or sin is not None:
+        raise ValueError("cos and sin must be given together")
     if positions is not None:
         _flat(positions, "positions", T, dev, torch.int64)
     if style not in ROPE_STYLES:
         raise ValueError(f"style must be one of {sorted(ROPE_STYLES)}")
     return (q.data_ptr(), Hq, ldq, hsq, k.data_ptr(), Hk, ldk, hsk, dt, T, D, _opt(q_weight), _opt(k_weight),
-            MXQ_BF16 if w_dt == torch.bfloat16 else MXQ_F32, eps, _opt(cos), _opt(sin), ldt, rows, rot,
+            MXQ_BF16 if w_dt == torch.bfloat16 else MXQ_F32, eps, _opt(cos), _opt(sin), ldt, rows, 2 * rot,
             _opt(positions), ROPE_STYLES[style])
 
 
-def _head_out(x, out, name, dtype):
+def _head_out(x, out, name):
     if out is None:
-        out = torch.empty(x.shape, dtype=dtype, device=x.device)
-    return out, _heads(out, name, dtype, x.device, x.shape)
+        T, H, D = x.shape
+        return torch.empty((T, H, D), dtype=x.dtype, device=x.device), (H * D, D)
+    return out, _heads(out, name, x.dtype, x.device, x.shape)
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions=None, eps=1e-6, style="interleaved", out_q=None,
@@ -665,8 +679,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions=None, eps=1e-6, s
     "interleaved" (2i, 2i+1) or "halves" (i, i + R/2).  Returns (q, k) of the input's type; ``out_q=q`` and
     ``out_k=k`` work in place."""
     args = _qk_inputs(q, k, q_weight, k_weight, cos, sin, positions, eps, style)
-    out_q, (ldq, hsq) = _head_out(q, out_q, "out_q", q.dtype)
-    out_k, (ldk, hsk) = _head_out(k, out_k, "out_k", q.dtype)
+    out_q, (ldq, hsq) = _head_out(q, out_q, "out_q")
+    out_k, (ldk, hsk) = _head_out(k, out_k, "out_k")
     _call(lib.mxq_qk_norm_rope, q.device, *args, out_q.data_ptr(), ldq, hsq, out_k.data_ptr(), ldk, hsk)
     return out_q, out_k
 
