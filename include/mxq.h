@@ -408,7 +408,8 @@ typedef enum {
  *           no other overlap.
  * head_dim: a multiple of 8 up to 512; rot_dim: a multiple of 8 up to head_dim; heads up
  *           to 65536 each.  Bases 16-byte aligned; all pitches of q, k, out_q, out_k
- *           multiples of 16 bytes and not negative; ld_table % 4 == 0.
+ *           multiples of 16 bytes and not negative; ld_table % 4 == 0.  The heads of one
+ *           token and 16 more at that pitch span less than 2^31 bytes.
  */
 mxq_status mxq_qk_norm_rope(const void* q, int64_t heads_q, int64_t ld_q, int64_t hs_q, const void* k,
                             int64_t heads_k, int64_t ld_k, int64_t hs_k, mxq_dtype dt, int64_t tokens,

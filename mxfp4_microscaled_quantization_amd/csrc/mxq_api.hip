@@ -161,6 +161,10 @@ mxq_status check_heads(const char* fn, const HeadArgs& h, int bytes, int out_byt
   if (h.ld < 0 || h.hs < 0 || h.ld_o < 0 || h.hs_o < 0 || !pitch_ok(h.ld) || !pitch_ok(h.hs) || !pitch_ok(h.ld_o) ||
       !pitch_ok(h.hs_o))
     return fail(MXQ_ERR_INVALID_ARG, "%s: pitches of %s must be 0 to 2^32 - 1", fn, h.name);
+  // offsets inside a token, those of the 16 heads that the last set may reach past its end
+  // included, stay below 2^31
+  if (h.heads > 1 && ((h.heads + 16) * h.hs * bytes >= (int64_t)1 << 31 || (h.heads + 16) * h.hs_o * out_bytes >= (int64_t)1 << 31))
+    return fail(MXQ_ERR_INVALID_ARG, "%s: the heads of a token in %s span too far (2^31 bytes with 16 more)", fn, h.name);
   if (!h.x || !h.out) return fail(MXQ_ERR_INVALID_ARG, "%s: %s or its output is NULL", fn, h.name);
   if (!aligned(h.x, 16) || h.ld * bytes % 16 != 0 || h.hs * bytes % 16 != 0)
     return fail(MXQ_ERR_INVALID_ARG, "%s: %s base and pitches must be 16-byte aligned", fn, h.name);
@@ -211,8 +215,10 @@ mxq_status qk_norm_rope(const char* fn, HeadArgs q, HeadArgs k, mxq_dtype dt, in
                   (long long)table_rows);
     if (!aligned(positions, 8)) return fail(MXQ_ERR_INVALID_ARG, "%s: positions must be 8-byte aligned", fn);
   }
-  auto side = [](const HeadArgs& h) {
-    return mxq::QkSide{h.x, h.heads > 0 ? h.w : nullptr, h.out, h.scales, h.ld, h.hs, h.ld_o, h.hs_o, h.ld_s, (int)h.heads};
+  auto side = [&](const HeadArgs& h) {
+    const bool many = h.heads > 1;   // a single head has no head pitch
+    return mxq::QkSide{h.x, h.heads > 0 ? h.w : nullptr, h.out, h.scales, h.ld, many ? h.hs : head_dim, h.ld_o,
+                       many ? h.hs_o : head_dim, h.ld_s, (int)h.heads};
   };
   mxq::QkNormParams p;
   p.q = side(q);

@@ -79,6 +79,7 @@ INVALID = [
     (_qk, dict(hq=-1), "heads_q"), (_qk, dict(hk=65537), "heads_k"), (_qk, dict(q=None), "q or its output"),
     (_qk, dict(ok=None), "k or its output"), (_qk, dict(q=ODD8), "16-byte"), (_qk, dict(ldq=252), "16-byte"),
     (_qk, dict(hsk=68), "16-byte"), (_qk, dict(ldk=-8), "pitches"), (_qk, dict(hsq=BIG), "pitches"), (_qk, dict(oq=ODD8), "16-byte"),
+    (_qk, dict(hq=3, hsq=2 ** 30), "span"), (_qk, dict(hq=3, hoq=2 ** 30, loq=2 ** 31), "span"),
     (_qk, dict(loq=32), "below head_dim"), (_qk, dict(hoq=32), "below head_dim"), (_qk, dict(wq=ODD2), "w_q"),
     (_qk, dict(wk=ODD8, wdt=0), "w_k"), (_qk, dict(eps=-1.0), "eps"), (_qk, dict(eps=float("nan")), "eps"),
     (_qk, dict(eps=float("inf")), "eps"), (_qk, dict(cos=None), "cos and sin"), (_qk, dict(sin=ODD8), "cos and sin"),

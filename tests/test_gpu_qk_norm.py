@@ -147,6 +147,57 @@ def test_degenerate_heads(gpu):
     assert int(qs.isnan().sum()) == 2
 
 
+def test_results_do_not_depend_on_the_batch(gpu):
+    """A token gives the same bits alone, among a few and among many (other variants of the
+    kernel), in every layout; and the same twice."""
+    announce("qk_norm_rope batch invariance")
+    T = 3000
+    for dtype, D, R, Hq, Hk in ((BF16, 128, 128, 40, 40), (F32, 96, 64, 12, 3), (BF16, 256, 256, 8, 8), (BF16, 64, 64, 24, 24)):
+        for style in ("interleaved", "halves"):
+            _, q, k, wq, wk, cos, sin, pos = _inputs(T, Hq, Hk, D, R, 100, dtype, dtype, 9)
+            kw = dict(eps=1e-6, style=style)
+            full = gpu.qk_norm_rope(q, k, wq, wk, cos, sin, positions=pos, **kw)
+            full8 = gpu.quantize_qk_norm_rope(q, k, wq, wk, cos, sin, positions=pos, **kw)
+            for _ in range(3):
+                again = gpu.qk_norm_rope(q, k, wq, wk, cos, sin, positions=pos, **kw)
+                assert all(torch.equal(a, b) for a, b in zip(again, full))
+            for lo, hi in ((0, 1), (17, 18), (100, 400), (1000, 1600)):
+                part = gpu.qk_norm_rope(q[lo:hi], k[lo:hi], wq, wk, cos, sin, positions=pos[lo:hi], **kw)
+                part8 = gpu.quantize_qk_norm_rope(q[lo:hi], k[lo:hi], wq, wk, cos, sin, positions=pos[lo:hi], **kw)
+                assert all(torch.equal(a, b[lo:hi]) for a, b in zip(part, full))
+                assert all(torch.equal(a, b[lo:hi]) for a, b in zip(part8, full8))
+
+
+def test_one_head_with_any_head_pitch(gpu):
+    """A single head has no head pitch: a huge one through the C ABI changes nothing and
+    writes nothing else."""
+    announce("qk_norm_rope one head, huge head pitch")
+    x = torch.randn(5, 1, 64, device="cuda")
+    ref, _ = gpu.qk_norm_rope(x, x[:, :0], None, None, None, None)
+    out = torch.full((7, 64), -3.0, device="cuda")
+    st = torch.cuda.current_stream().cuda_stream
+    for hs in (0, 1 << 29, 1 << 31):
+        out.fill_(-3.0)
+        assert gpu.lib.mxq_qk_norm_rope(x.data_ptr(), 1, 64, hs, None, 0, 0, 0, 0, 5, 64, None, None, 0, 1e-6, None, None, 0, 0,
+                                        0, None, 0, out[1:].data_ptr(), 64, max(hs, 64), None, 0, 0, st) == 0
+        assert torch.equal(out[1:6], ref[:, 0]) and (out[0] == -3).all() and (out[6] == -3).all()
+
+
+def test_shared_and_many_heads(gpu):
+    """Inputs whose heads are one and the same (head pitch 0), and more heads than a grid row
+    has workgroups for."""
+    announce("qk_norm_rope shared heads")
+    for T in (3, 600):
+        x = torch.randn(T, 1, 128, device="cuda").to(BF16)
+        one, _ = gpu.qk_norm_rope(x, x[:, :0], None, None, None, None)
+        many, _ = gpu.qk_norm_rope(x.expand(T, 9, 128), x[:, :0], None, None, None, None)
+        assert torch.equal(many, one.expand(T, 9, 128))
+    x = torch.randn(2, 40000, 512, device="cuda").to(BF16)
+    q, k = gpu.qk_norm_rope(x, x, None, None, None, None)
+    assert torch.equal(q, k)
+    _check(q[:, ::1777], *_oracle(x[:, ::1777], None, None, None, None, 1e-6, "halves"))
+
+
 def test_empty(gpu):
     announce("qk_norm_rope empty")
     e = torch.empty(0, 3, 64, device="cuda")
