@@ -5,7 +5,10 @@
 // its first code, so a row is held in registers between the two: T = 64 W threads take
 // one row, C units of 8 elements each, all loads first, one reduction (DPP inside a wave,
 // LDS across the W waves), then the codes.  Rows past T * 8 * C elements of the largest
-// variant are read twice.
+// variant are read twice; rows of up to 32 units (heads) share a wave.
+// Measured: 75600 x 13824 bf16 0.51 ms (6.1 TB/s; a row over 4 waves x 8 units 0.52, over
+// 16 x 2 0.57), 75600 x 5120 0.18 ms (6.4 TB/s), 300000 x 128 0.0185 ms (6.2 TB/s; a
+// wave for each row 0.058); dequantization of 300000 x 128 0.018 ms (6.4 TB/s).
 #include <type_traits>
 
 #include "mxq_int8.hpp"
@@ -22,15 +25,17 @@ template <bool F32> struct Unit {
   v4i d[F32 ? 2 : 1];
 };
 
-template <bool F32>
+// STREAM: loads past the caches, for inputs that do not fit them (see launch_quantize_int8)
+template <bool F32, bool STREAM>
 __device__ __forceinline__ Unit<F32> load_unit(const void* x, int64_t elem) {
+  auto get = [](const v4i* p) { return STREAM ? __builtin_nontemporal_load(p) : *p; };
   Unit<F32> u;
   if constexpr (F32) {
     const v4i* p = reinterpret_cast<const v4i*>(static_cast<const float*>(x) + elem);
-    u.d[0] = __builtin_nontemporal_load(p);
-    u.d[1] = __builtin_nontemporal_load(p + 1);
+    u.d[0] = get(p);
+    u.d[1] = get(p + 1);
   } else {
-    u.d[0] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(static_cast<const uint16_t*>(x) + elem));
+    u.d[0] = get(reinterpret_cast<const v4i*>(static_cast<const uint16_t*>(x) + elem));
   }
   return u;
 }
@@ -78,7 +83,7 @@ __device__ __forceinline__ v2u unit_codes(const Unit<F32>& u, const Int8Scale& s
 
 // W waves per row; C units per thread held in registers.  Workgroups of max(W, 4) waves:
 // with W == 1 each of the four waves has a row of its own and nothing is synchronized.
-template <bool F32, int W, int C>
+template <bool F32, bool STREAM, int W, int C>
 __global__ __launch_bounds__(64 * (W < 4 ? 4 : W)) void int8_quantize_kernel(
     const void* __restrict__ x, int64_t rows, uint32_t units, int64_t ld_x, int8_t* __restrict__ codes,
     int64_t ld_codes, float* __restrict__ scales) {
@@ -92,7 +97,7 @@ __global__ __launch_bounds__(64 * (W < 4 ? 4 : W)) void int8_quantize_kernel(
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const uint32_t i = c * T + tid;
-      u[c] = i < units ? load_unit<F32>(x, row * ld_x + (int64_t)i * 8) : zero_unit<F32>();
+      u[c] = i < units ? load_unit<F32, STREAM>(x, row * ld_x + (int64_t)i * 8) : zero_unit<F32>();
     }
     unsigned m = 0;
 #pragma unroll
@@ -117,6 +122,39 @@ __global__ __launch_bounds__(64 * (W < 4 ? 4 : W)) void int8_quantize_kernel(
   }
 }
 
+// Rows of up to G units, 64 / G of them in a wave: lane l of a group has unit l, R rows of
+// each group in flight.
+template <bool F32, bool STREAM, int G>
+__global__ __launch_bounds__(256) void int8_quantize_short_kernel(const void* __restrict__ x, int64_t rows,
+                                                                  uint32_t units, int64_t ld_x,
+                                                                  int8_t* __restrict__ codes, int64_t ld_codes,
+                                                                  float* __restrict__ scales) {
+  constexpr int PER = 256 / G, R = 4;   // rows of the workgroup at once, passes in flight
+  const uint32_t l = threadIdx.x % G;
+  const bool own = l < units;
+  for (int64_t r0 = (int64_t)blockIdx.x * (PER * R) + threadIdx.x / G; r0 < rows; r0 += (int64_t)gridDim.x * (PER * R)) {
+    Unit<F32> u[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const int64_t row = r0 + k * PER;
+      u[k] = own && row < rows ? load_unit<F32, STREAM>(x, row * ld_x + (int64_t)l * 8) : zero_unit<F32>();
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const int64_t row = r0 + k * PER;
+      unsigned m = unit_max<F32>(u[k]);
+      m = G == 8 ? row8_max_u32(m) : row16_max_u32(m);
+      if constexpr (G == 32) m = max(m, (unsigned)__shfl_xor((int)m, 16));
+      const Int8Scale sc = int8_scale(m);
+      if (row < rows) {
+        if (l == 0) scales[row] = sc.s;
+        if (own)
+          __builtin_nontemporal_store(unit_codes<F32>(u[k], sc), reinterpret_cast<v2u*>(codes + row * ld_codes + (int64_t)l * 8));
+      }
+    }
+  }
+}
+
 // Rows longer than the registers of 16 waves hold: the second reading comes from the caches.
 template <bool F32>
 __global__ __launch_bounds__(1024) void int8_quantize_long_kernel(const void* __restrict__ x, int64_t rows,
@@ -128,7 +166,7 @@ __global__ __launch_bounds__(1024) void int8_quantize_long_kernel(const void* __
   int par = 0;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, par ^= 1) {
     unsigned m = 0;
-    for (uint32_t i = tid; i < units; i += 1024) m = max(m, unit_max<F32>(load_unit<F32>(x, row * ld_x + (int64_t)i * 8)));
+    for (uint32_t i = tid; i < units; i += 1024) m = max(m, unit_max<F32>(load_unit<F32, false>(x, row * ld_x + (int64_t)i * 8)));
     m = wave_max_u32(m);
     if ((tid & 63) == 0) red[par][tid >> 6] = m;
     __syncthreads();
@@ -138,7 +176,7 @@ __global__ __launch_bounds__(1024) void int8_quantize_long_kernel(const void* __
     if (tid == 0) scales[row] = sc.s;
     for (uint32_t i = tid; i < units; i += 1024)
       *reinterpret_cast<v2u*>(codes + row * ld_codes + (int64_t)i * 8) =
-          unit_codes<F32>(load_unit<F32>(x, row * ld_x + (int64_t)i * 8), sc);
+          unit_codes<F32>(load_unit<F32, false>(x, row * ld_x + (int64_t)i * 8), sc);
   }
 }
 
@@ -190,27 +228,39 @@ hipError_t launch_quantize_int8(const void* x, bool f32, int64_t rows, int64_t c
     hipLaunchKernelGGL(kernel, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(threads), 0, stream, x, rows, units,
                        ld_x, codes, ld_codes, scales);
   };
-  auto pick = [&](auto f_tag) {
-    constexpr bool F = decltype(f_tag)::value;
-    if (units <= 64)
-      go(int8_quantize_kernel<F, 1, 1>, 256, 4);
+  auto pick = [&](auto f_tag, auto s_tag) {
+    constexpr bool F = decltype(f_tag)::value, S = decltype(s_tag)::value;
+    if (units <= 8)
+      go(int8_quantize_short_kernel<F, S, 8>, 256, 32 * 4);
+    else if (units <= 16)
+      go(int8_quantize_short_kernel<F, S, 16>, 256, 16 * 4);
+    else if (units <= 32)
+      go(int8_quantize_short_kernel<F, S, 32>, 256, 8 * 4);
+    else if (units <= 64)
+      go(int8_quantize_kernel<F, S, 1, 1>, 256, 4);
     else if (units <= 128)
-      go(int8_quantize_kernel<F, 1, 2>, 256, 4);
+      go(int8_quantize_kernel<F, S, 1, 2>, 256, 4);
     else if (units <= 256)
-      go(int8_quantize_kernel<F, 1, 4>, 256, 4);
+      go(int8_quantize_kernel<F, S, 1, 4>, 256, 4);
     else if (units <= 256 * 4)
-      go(int8_quantize_kernel<F, 4, 4>, 256, 1);
-    else if (units <= 256 * 8)
-      go(int8_quantize_kernel<F, 4, 8>, 256, 1);
+      go(int8_quantize_kernel<F, S, 4, 4>, 256, 1);
+    else if (units <= 512 * 4)
+      go(int8_quantize_kernel<F, S, 8, 4>, 512, 1);
     else if (units <= 1024 * 8)
-      go(int8_quantize_kernel<F, 16, 8>, 1024, 1);
+      go(int8_quantize_kernel<F, S, 16, 8>, 1024, 1);
     else
       go(int8_quantize_long_kernel<F>, 1024, 1);
   };
+  // An input that fits the 256 MB of memory-side cache may be there still from the kernel
+  // that wrote it, and ordinary loads find it (20000 x 5120 bf16: 43 us, 47 with streaming
+  // loads); a larger one is only slowed down by passing through (75600 x 5120: 200 and 180 us).
+  const bool stream_loads = rows * cols * (f32 ? 4 : 2) > ((int64_t)256 << 20);
+  using T = std::true_type;
+  using N = std::false_type;
   if (f32)
-    pick(std::true_type{});
+    stream_loads ? pick(T{}, T{}) : pick(T{}, N{});
   else
-    pick(std::false_type{});
+    stream_loads ? pick(N{}, T{}) : pick(N{}, N{});
   return hipGetLastError();
 }
 

@@ -55,11 +55,14 @@ __device__ __forceinline__ unsigned int8_pack4(float x0, float x1, float x2, flo
 // max |x| of the two bf16 in a word, as bf16 patterns in both halves
 __device__ __forceinline__ v2h abs_bf16x2(int pair) { return __builtin_bit_cast(v2h, (unsigned)pair & 0x7FFF7FFFu); }
 
-// Max over the 64 lanes of a wave, in every lane: DPP inside each row of 16, then two
-// lane swaps across rows.
-__device__ __forceinline__ unsigned row16_max_u32(unsigned v) {
+// Max over each 8 or 16 lanes, or the 64 lanes of a wave, in every lane: DPP inside a row of
+// 16, then two lane swaps across rows.
+__device__ __forceinline__ unsigned row8_max_u32(unsigned v) {
   v = quad_max_u32(v);
-  v = max(v, (unsigned)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, false));  // row_half_mirror
+  return max(v, (unsigned)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, false));  // row_half_mirror
+}
+__device__ __forceinline__ unsigned row16_max_u32(unsigned v) {
+  v = row8_max_u32(v);
   v = max(v, (unsigned)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, false));  // row_mirror
   return v;
 }
