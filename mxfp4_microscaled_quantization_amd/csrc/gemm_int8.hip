@@ -364,18 +364,53 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(I8Params p) {
       return;
     }
   }
+  // binary32 outputs, and rows that are not 16-byte aligned or end inside the tile: the same
+  // through a binary32 image of CJ blocks of rows, stored in the order of the rows (single
+  // elements where a row has no alignment: 1001 x 1360 x 2051 to binary32 took 17.2 us with
+  // each lane storing its own columns, 14.8 here)
+  constexpr int PITCH = 16 * MI + 4;               // floats per row in LDS
+  constexpr int FIT = (int)(sizeof(lds) / (WAVES * 16 * PITCH * 4));
+  constexpr int CJ = FIT >= MJ ? MJ : FIT >= 4 ? 4 : FIT >= 2 ? 2 : 1;
+  static_assert(FIT >= 1 && MJ % CJ == 0, "whole passes");
+  __syncthreads();
+  float* sub = reinterpret_cast<float*>(lds) + wave * (CJ * 16 * PITCH);
+  const bool whole = OUT == OUT_F32 && p.vec && n0 + BN <= p.N;
 #pragma unroll
-  for (int j = 0; j < MJ; ++j) {
-    const int m = mw + (int)(16 * j + r16);
-    if (m >= p.M) continue;
-    const float sa = p.a_scales[m * p.inc_as];
+  for (int jb = 0; jb < MJ; jb += CJ) {
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const int n = nw + 16 * i + 4 * (int)g;
-      float v[4];
+    for (int j = 0; j < CJ; ++j) {
+      const float sa = p.a_scales[min(mw + 16 * (jb + j) + (int)r16, p.M - 1) * p.inc_as];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = scaled(acc[i][j][e], sa, sw[i][e], bs[i][e], has_bias);
-      store_channels<OUT == OUT_F32>(p, m, n, v, p.vec && n + 4 <= p.N);
+      for (int i = 0; i < MI; ++i) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = scaled(acc[i][jb + j][e], sa, sw[i][e], bs[i][e], has_bias);
+        *reinterpret_cast<v4f*>(sub + (16 * j + r16) * PITCH + 16 * i + 4 * g) = v4f{v[0], v[1], v[2], v[3]};
+      }
+    }
+    const int mb = mw + 16 * jb;
+    if (whole) {
+      constexpr int LPR = 4 * MI;                  // lanes per row, 4 columns each
+#pragma unroll
+      for (int q = 0; q < 16 * CJ * LPR / 64; ++q) {
+        const int row = (int)(64 * q + lane) / LPR, col = (int)(64 * q + lane) % LPR * 4;
+        const v4f v = *reinterpret_cast<const v4f*>(sub + row * PITCH + col);
+        if (mb + row < p.M)
+          __builtin_nontemporal_store(v, reinterpret_cast<v4f*>(static_cast<float*>(p.out) + (int64_t)(mb + row) * p.ld_out + nw + col));
+      }
+    } else {
+#pragma unroll 4
+      for (int q = 0; q < 16 * CJ * 16 * MI / 64; ++q) {
+        const int row = (int)(64 * q + lane) / (16 * MI), col = (int)(64 * q + lane) % (16 * MI);
+        const float v = sub[row * PITCH + col];
+        if (mb + row < p.M && nw + col < p.N) {
+          const int64_t at = (int64_t)(mb + row) * p.ld_out + nw + col;
+          if constexpr (OUT == OUT_F32)
+            static_cast<float*>(p.out)[at] = v;
+          else
+            static_cast<uint16_t*>(p.out)[at] = (uint16_t)pack_bf16x2(v, 0.0f);
+        }
+      }
     }
   }
 }
