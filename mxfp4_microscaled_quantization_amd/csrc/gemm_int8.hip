@@ -522,18 +522,24 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_i8_few_kernel(I8Params p) {
 
 // ---------------------------------------------------------------------------------
 // Choice of the tile, and of a split of K.  Every kernel gives the same sums, so this is
-// about time alone: one round of up to 256 tiles (one for each CU) takes fixed + per_window
-// * windows us with the tile in question (measured with cold operands at K = 5120 and
-// 13824), a split of K adds the reduction and its traffic.  A small tile wins until the
-// larger one fills the CUs; past that the largest tile's reuse does.
+// about time alone.  A round of up to 256 tiles (one for each CU) takes fixed + per_window
+// * windows us with the tile in question, kLaunch of it once; a further round takes `again`
+// of the first (less than 1 where two workgroups fit a CU); a split of K adds the reduction
+// and its traffic.  The constants are fits to times with cold operands, K = 5120 and 13824.
+// So a small tile is taken until a larger one fills the CUs, and the largest past that:
+//   512 x 5120 x 5120: 256 x 256 58 us, 128 x 256 40, 128 x 128 28, 64 x 128 40, 64 x 64 34
+//   2048 x 5120 x 5120: 57, 78, 79, 99, 102;  128 x 5120 x 5120: 60, 43, 29, 22, 15.5
+//   64 x 13824 x 5120: 64 x 32 27.5, 64 x 64 36, 64 x 64 in 3 parts of K 20.6
 struct TileCost {
   int bm, bn;
-  float fixed, per_window;
+  float fixed, per_window, again;
 };
+constexpr float kLaunch = 3.0f;
 enum { TILE_256x256, TILE_128x256, TILE_128x128, TILE_64x128, TILE_128x64, TILE_64x64, TILE_64x32, TILE_32x64, TILE_32x32, TILES };
 constexpr TileCost kTileCost[TILES] = {
-    {256, 256, 12.2f, 1.156f}, {128, 256, 11.7f, 0.728f}, {128, 128, 6.5f, 0.537f}, {64, 128, 5.8f, 0.404f}, {128, 64, 5.8f, 0.404f},
-    {64, 64, 4.2f, 0.288f},    {64, 32, 4.0f, 0.222f},    {32, 64, 4.0f, 0.225f},   {32, 32, 3.2f, 0.162f}};
+    {256, 256, 12.2f, 1.156f, 1.0f}, {128, 256, 11.7f, 0.728f, 1.0f}, {128, 128, 6.5f, 0.537f, 1.0f},
+    {64, 128, 5.8f, 0.404f, 1.0f},   {128, 64, 5.8f, 0.404f, 1.0f},   {64, 64, 4.2f, 0.288f, 0.75f},
+    {64, 32, 4.0f, 0.222f, 0.75f},   {32, 64, 4.0f, 0.225f, 0.75f},   {32, 32, 3.2f, 0.162f, 0.75f}};
 constexpr int kFewTokens = 8;
 
 struct Plan {
@@ -549,8 +555,8 @@ Plan plan_w8a8(int64_t M, int64_t N, int64_t K, bool may_split) {
     if (t != TILE_256x256 && tiles > ((int64_t)1 << 22)) continue;   // threads of a launch stay below 2^32
     for (int s = 1; s <= (may_split ? 8 : 1); ++s) {
       if (s > 1 && (tiles * s > 256 || nwin < 8 * s)) break;
-      const double rounds = (double)((tiles * s + 255) / 256);
-      double us = c.fixed + c.per_window * (double)((nwin + s - 1) / s) * rounds;
+      const double further = (double)((tiles * s + 255) / 256 - 1);
+      double us = kLaunch + (c.fixed - kLaunch + c.per_window * (double)((nwin + s - 1) / s)) * (1.0 + c.again * further);
       if (s > 1) us += 4.5 + (double)s * (double)M * (double)N * 8.0 / 5e6;
       if (least == 0 || us < least) {
         least = us;
