@@ -34,6 +34,8 @@ struct I8Params {
   const float* w_scales;
   const float* bias;       // or null
   void* out;
+  const void* x;           // unquantized activations, and their row pitch in elements
+  int64_t ld_x;
   int64_t ld_out, inc_as, inc_ws;
   int M, N, K;
   uint32_t ld_a, ld_w;
@@ -442,12 +444,28 @@ __global__ __launch_bounds__(256) void i8_reduce_kernel(I8Params p) {
 // sums meet (integers: the order changes nothing).  The workgroups start at windows spread
 // over K: started together, they would read the same columns of all rows at once, which a
 // row pitch of a power of two maps to a few memory channels (1 x 8192 x 4096: 12.0 -> 9.0 us).
-template <int NI, int WAVES, int D, bool F32OUT>
+//
+// A_BF16, A_F32: the activations come unquantized, and every workgroup makes the codes of
+// all tokens itself, into LDS, while its first weight windows are on their way: at a few KB
+// that costs less than a launch of its own.
+enum { A_CODES = 0, A_BF16 = 1, A_F32 = 2 };
+constexpr int kFewTokens = 8;
+constexpr uint32_t kFewCodes = 15872;              // bytes of codes that a workgroup holds: two fit a CU
+
+__device__ __host__ constexpr uint32_t few_pitch(int nwin) { return (uint32_t)nwin * kWin + 16u; }
+
+template <int NI, int WAVES, int D, int A, bool F32OUT>
 __global__ __launch_bounds__(64 * WAVES) void gemm_i8_few_kernel(I8Params p) {
-  constexpr int LINES = 2 * NI + 1;                // 1 KB lines of 8 rows: weights, then activations
+  constexpr int LINES = 2 * NI + (A == A_CODES ? 1 : 0);   // 1 KB lines of 8 rows: weights, then activations
   constexpr uint32_t SLOT = LINES * 1024;
+  constexpr int T = 64 * WAVES;
   static_assert((D - 1) * LINES < 64, "vmcnt range");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[WAVES * D * SLOT];
+  // one array for everything: with several, the compiler orders every read of LDS behind all
+  // loads into it
+  constexpr uint32_t RING = WAVES * D * SLOT, CODES = A == A_CODES ? 0 : kFewCodes;
+  constexpr uint32_t SMALL = A == A_CODES ? 0 : 4 * kFewTokens * (3 + WAVES);
+  static_assert(RING + CODES + SMALL <= 81920, "two workgroups on a CU");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[RING + CODES + SMALL];
   const uint32_t tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)(tid >> 6));
   const int n0 = (int)blockIdx.x * (16 * NI);
@@ -459,22 +477,90 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_i8_few_kernel(I8Params p) {
   const uint32_t drow = lane >> 3, dslot = lane & 7;   // as in gemm_i8_kernel
   const uint32_t chunk0 = (dslot ^ ((drow >> 1) & 7u)) * 16, chunk1 = (dslot ^ (((8u + drow) >> 1) & 7u)) * 16;
   uint8_t* ring = lds + (uint32_t)wave * (D * SLOT);
+  auto window = [&](int w) { return w + start >= nwin ? w + start - nwin : w + start; };
   auto issue = [&](int w, uint32_t slot) {
-    const int k = w + start >= nwin ? w + start - nwin : w + start;
+    const int k = window(w);
     const __amdgpu_buffer_rsrc_t rw = make_rsrc(base_w, w < nwin ? bytes_w : 0u);
 #pragma unroll
     for (int j = 0; j < 2 * NI; ++j)
       line_to_lds(rw, ring + slot * SLOT + j * 1024, drow * p.ld_w + ((j & 1) ? chunk1 : chunk0),
                   (uint32_t)k * kWin + j * 8 * p.ld_w);
-    const uint32_t valid = k + 1 < nwin ? (uint32_t)kWin : last_bytes;
-    line_to_lds(make_rsrc(p.a, w < nwin ? bytes_a : 0u), ring + slot * SLOT + 2 * NI * 1024,
-                chunk0 < valid ? drow * p.ld_a + chunk0 : kOutside, (uint32_t)k * kWin);
+    if constexpr (A == A_CODES) {
+      const uint32_t valid = k + 1 < nwin ? (uint32_t)kWin : last_bytes;
+      line_to_lds(make_rsrc(p.a, w < nwin ? bytes_a : 0u), ring + slot * SLOT + 2 * NI * 1024,
+                  chunk0 < valid ? drow * p.ld_a + chunk0 : kOutside, (uint32_t)k * kWin);
+    }
   };
+
+  // the codes of all tokens, rows few_pitch apart, and their scales
+  uint8_t* codes = lds + RING;
+  float* scales = reinterpret_cast<float*>(codes + CODES);
+  float* invs = scales + kFewTokens;
+  unsigned* keeps = reinterpret_cast<unsigned*>(invs + kFewTokens);
+  unsigned* red = keeps + kFewTokens;                      // [kFewTokens][WAVES]
+  const uint32_t pitch = few_pitch(nwin);
+  if constexpr (A != A_CODES) {
+    constexpr bool F32 = A == A_F32;
+    constexpr int C = (int)(kFewCodes / 8 + T - 1) / T;     // units of 8 elements per thread
+    const uint32_t upr = (uint32_t)p.K / 8, total = upr * (uint32_t)p.M;
+    Unit<F32> u[C];
+    uint32_t row[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const uint32_t i = c * T + tid;
+      row[c] = 0;
+      for (int m = 1; m < p.M; ++m) row[c] += i >= (uint32_t)m * upr ? 1u : 0u;
+      u[c] = i < total ? load_unit<F32, false>(p.x, (int64_t)row[c] * p.ld_x + (i - row[c] * upr) * 8) : zero_unit<F32>();
+    }
+    // the loads above are older than these: they are waited for alone
+#pragma unroll
+    for (int d = 0; d < D; ++d) issue(wave + d * WAVES, d);
+    unsigned most[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) most[c] = unit_max<F32>(u[c]);
+    for (int m = 0; m < p.M; ++m) {
+      unsigned v = 0;
+#pragma unroll
+      for (int c = 0; c < C; ++c) v = max(v, row[c] == (uint32_t)m ? most[c] : 0u);
+      v = wave_max_u32(v);
+      if (lane == 0) red[m * WAVES + wave] = v;
+    }
+    __builtin_amdgcn_s_waitcnt(wait_vm(63));               // the LDS writes; the weights stay in flight
+    handover_barrier();
+    if (tid < (uint32_t)p.M) {
+      unsigned v = 0;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) v = max(v, red[tid * WAVES + w]);
+      const Int8Scale sc = int8_scale(v);
+      scales[tid] = sc.s;
+      invs[tid] = sc.inv;
+      keeps[tid] = sc.keep;
+    }
+    __builtin_amdgcn_s_waitcnt(wait_vm(63));
+    handover_barrier();
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const uint32_t i = c * T + tid;
+      if (i < total) {
+        const Int8Scale sc = {0.0f, invs[row[c]], keeps[row[c]]};
+        *reinterpret_cast<v2u*>(codes + row[c] * pitch + (i - row[c] * upr) * 8) = unit_codes<F32>(u[c], sc);
+      }
+    }
+    // zeros from K to the end of the last window
+    if (tid < 8u * (uint32_t)p.M) {
+      const uint32_t k = (uint32_t)(nwin - 1) * kWin + (tid & 7) * 16;
+      if (nwin > 0 && k >= (uint32_t)p.K) *reinterpret_cast<v4i*>(codes + (tid >> 3) * pitch + k) = v4i{0, 0, 0, 0};
+    }
+    __builtin_amdgcn_s_waitcnt(wait_vm(63));
+    handover_barrier();
+  } else {
+#pragma unroll
+    for (int d = 0; d < D; ++d) issue(wave + d * WAVES, d);
+  }
+
   v4i acc[NI];
 #pragma unroll
   for (int i = 0; i < NI; ++i) acc[i] = v4i{0, 0, 0, 0};
-#pragma unroll
-  for (int d = 0; d < D; ++d) issue(wave + d * WAVES, d);
   uint32_t slot = 0;
   for (int w = wave; w < nwin; w += WAVES) {
     __builtin_amdgcn_s_waitcnt(wait_vm((D - 1) * LINES));   // window w landed
@@ -485,8 +571,11 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_i8_few_kernel(I8Params p) {
     for (int t = 0; t < 2; ++t) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) fw[t][i] = *reinterpret_cast<const v4i*>(s + lds_slot(16 * i + r16, g + 4 * t));
-      // tokens 8 .. 15 of the product are not used: they repeat 0 .. 7
-      fa[t] = *reinterpret_cast<const v4i*>(s + NI * 2048 + lds_slot(r16 & 7, g + 4 * t));
+      // columns of the product past the tokens are not used: they repeat others
+      if constexpr (A == A_CODES)
+        fa[t] = *reinterpret_cast<const v4i*>(s + NI * 2048 + lds_slot(r16 & 7, g + 4 * t));
+      else
+        fa[t] = *reinterpret_cast<const v4i*>(codes + min(r16, (uint32_t)p.M - 1) * pitch + (uint32_t)window(w) * kWin + 64 * t + 16 * g);
     }
     __builtin_amdgcn_s_waitcnt(wait_vm(63));                // the reads are done: the slot can be refilled
     asm volatile("" ::: "memory");
@@ -504,7 +593,7 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_i8_few_kernel(I8Params p) {
   for (int i = 0; i < NI; ++i) part[(wave * NI + i) * 64 + lane] = acc[i];
   __syncthreads();
   // thread e: token e / (4 NI), 4 channels from 4 (e % (4 NI))
-  for (uint32_t e = tid; e < 4 * NI * (uint32_t)p.M; e += 64 * WAVES) {
+  for (uint32_t e = tid; e < 4 * NI * (uint32_t)p.M; e += T) {
     const uint32_t m = e / (4 * NI), q = e % (4 * NI);
     const int n = n0 + 4 * (int)q;
     if (n >= p.N) continue;
@@ -513,7 +602,7 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_i8_few_kernel(I8Params p) {
     for (int w = 0; w < WAVES; ++w) sum += part[(w * NI + (q >> 2)) * 64 + (q & 3) * 16 + m];
     float sw[4], bs[4], v[4];
     load_channels(p, n, sw, bs);
-    const float sa = p.a_scales[m * p.inc_as];
+    const float sa = A == A_CODES ? p.a_scales[m * p.inc_as] : scales[m];
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = scaled(sum[k], sa, sw[k], bs[k], p.bias != nullptr);
     store_channels<F32OUT>(p, (int)m, n, v, p.vec && n + 4 <= p.N);
@@ -540,8 +629,6 @@ constexpr TileCost kTileCost[TILES] = {
     {256, 256, 12.2f, 1.156f, 1.0f}, {128, 256, 11.7f, 0.728f, 1.0f}, {128, 128, 6.5f, 0.537f, 1.0f},
     {64, 128, 5.8f, 0.404f, 1.0f},   {128, 64, 5.8f, 0.404f, 1.0f},   {64, 64, 4.2f, 0.288f, 0.75f},
     {64, 32, 4.0f, 0.222f, 0.75f},   {32, 64, 4.0f, 0.225f, 0.75f},   {32, 32, 3.2f, 0.162f, 0.75f}};
-constexpr int kFewTokens = 8;
-
 struct Plan {
   int tile, splits;
 };
@@ -575,38 +662,69 @@ size_t gemm_w8a8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   return splits == 1 ? 0 : (size_t)splits * (size_t)M * (size_t)((N + 3) / 4 * 4) * 4;
 }
 
-hipError_t launch_gemm_w8a8(const int8_t* a, int64_t ld_a, const float* a_scales, int64_t inc_as, const int8_t* w,
-                            int64_t ld_w, const float* w_scales, int64_t inc_ws, const float* bias, int64_t M,
-                            int64_t N, int64_t K, void* out, bool f32_out, int64_t ld_out, void* workspace,
-                            hipStream_t stream) {
-  if (M == 0 || N == 0) return hipSuccess;
-  I8Params p;
-  p.a = a;
-  p.a_scales = a_scales;
+bool gemm_w8a8_one_launch(int64_t M, int64_t K) {
+  return M <= kFewTokens && M * (int64_t)few_pitch((int)((K + kWin - 1) / kWin)) <= (int64_t)kFewCodes;
+}
+
+namespace {
+
+// What does not depend on the activations.
+I8Params i8_params(const int8_t* w, int64_t ld_w, const float* w_scales, int64_t inc_ws, const float* bias, int64_t M,
+                   int64_t N, int64_t K, void* out, bool f32_out, int64_t ld_out) {
+  I8Params p = {};
   p.w = w;
   p.w_scales = w_scales;
   p.bias = bias;
   p.out = out;
   p.ld_out = ld_out;
-  p.inc_as = inc_as;
   p.inc_ws = inc_ws;
   p.M = (int)M;
   p.N = (int)N;
   p.K = (int)K;
-  p.ld_a = (uint32_t)ld_a;
   p.ld_w = (uint32_t)ld_w;
   p.nwin = (int)((K + kWin - 1) / kWin);
   auto aligned16 = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
   p.vec = (ld_out * (f32_out ? 4 : 2)) % 16 == 0 && aligned16(out);
   p.vec_channels = inc_ws == 1 && aligned16(w_scales) && aligned16(bias);
+  p.splits = 1;
+  return p;
+}
+
+template <int A>
+void launch_few(const I8Params& p, bool f32_out, hipStream_t stream) {
+  const dim3 grid((unsigned)(((int64_t)p.N + 31) / 32)), block(256);
+  if (f32_out)
+    hipLaunchKernelGGL((gemm_i8_few_kernel<2, 4, 4, A, true>), grid, block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((gemm_i8_few_kernel<2, 4, 4, A, false>), grid, block, 0, stream, p);
+}
+
+}  // namespace
+
+hipError_t launch_gemm_w8a8_unquantized(const void* x, bool f32, int64_t ld_x, const int8_t* w, int64_t ld_w,
+                                        const float* w_scales, int64_t inc_ws, const float* bias, int64_t M, int64_t N,
+                                        int64_t K, void* out, bool f32_out, int64_t ld_out, hipStream_t stream) {
+  I8Params p = i8_params(w, ld_w, w_scales, inc_ws, bias, M, N, K, out, f32_out, ld_out);
+  p.x = x;
+  p.ld_x = ld_x;
+  f32 ? launch_few<A_F32>(p, f32_out, stream) : launch_few<A_BF16>(p, f32_out, stream);
+  return hipGetLastError();
+}
+
+hipError_t launch_gemm_w8a8(const int8_t* a, int64_t ld_a, const float* a_scales, int64_t inc_as, const int8_t* w,
+                            int64_t ld_w, const float* w_scales, int64_t inc_ws, const float* bias, int64_t M,
+                            int64_t N, int64_t K, void* out, bool f32_out, int64_t ld_out, void* workspace,
+                            hipStream_t stream) {
+  if (M == 0 || N == 0) return hipSuccess;
+  I8Params p = i8_params(w, ld_w, w_scales, inc_ws, bias, M, N, K, out, f32_out, ld_out);
+  p.a = a;
+  p.a_scales = a_scales;
+  p.inc_as = inc_as;
+  p.ld_a = (uint32_t)ld_a;
   p.part = static_cast<int*>(workspace);
   p.ld_part = (int)((N + 3) / 4 * 4);
-  p.splits = 1;
   if (M <= kFewTokens) {
-    auto few = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, dim3((unsigned)((N + 31) / 32)), dim3(256), 0, stream, p);
-    };
-    f32_out ? few(gemm_i8_few_kernel<2, 4, 4, true>) : few(gemm_i8_few_kernel<2, 4, 4, false>);
+    launch_few<A_CODES>(p, f32_out, stream);
     return hipGetLastError();
   }
   const Plan plan = plan_w8a8(M, N, K, workspace != nullptr);

@@ -20,67 +20,6 @@ namespace {
 constexpr int kDqI8Threads = 1024;
 constexpr int kDqI8Unroll = 4;
 
-// 8 elements of a row as loaded: 16 bytes of bf16, or twice 16 bytes of binary32
-template <bool F32> struct Unit {
-  v4i d[F32 ? 2 : 1];
-};
-
-// STREAM: loads past the caches, for inputs that do not fit them (see launch_quantize_int8)
-template <bool F32, bool STREAM>
-__device__ __forceinline__ Unit<F32> load_unit(const void* x, int64_t elem) {
-  auto get = [](const v4i* p) { return STREAM ? __builtin_nontemporal_load(p) : *p; };
-  Unit<F32> u;
-  if constexpr (F32) {
-    const v4i* p = reinterpret_cast<const v4i*>(static_cast<const float*>(x) + elem);
-    u.d[0] = get(p);
-    u.d[1] = get(p + 1);
-  } else {
-    u.d[0] = get(reinterpret_cast<const v4i*>(static_cast<const uint16_t*>(x) + elem));
-  }
-  return u;
-}
-
-template <bool F32>
-__device__ __forceinline__ Unit<F32> zero_unit() {
-  Unit<F32> u;
-  u.d[0] = v4i{0, 0, 0, 0};
-  if constexpr (F32) u.d[1] = v4i{0, 0, 0, 0};
-  return u;
-}
-
-// max |x| of a unit as a binary32 pattern
-template <bool F32>
-__device__ __forceinline__ unsigned unit_max(const Unit<F32>& u) {
-  if constexpr (F32) {
-    unsigned m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, max((unsigned)u.d[0][i] & 0x7FFFFFFFu, (unsigned)u.d[1][i] & 0x7FFFFFFFu));
-    return m;
-  } else {
-    v2h m = abs_bf16x2(u.d[0][0]);
-#pragma unroll
-    for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, abs_bf16x2(u.d[0][i]));
-    return max((unsigned)m[0], (unsigned)m[1]) << 16;
-  }
-}
-
-template <bool F32>
-__device__ __forceinline__ v2u unit_codes(const Unit<F32>& u, const Int8Scale& sc) {
-  v2u o;
-  if constexpr (F32) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      o[h] = int8_pack4(__int_as_float(u.d[h][0]), __int_as_float(u.d[h][1]), __int_as_float(u.d[h][2]),
-                        __int_as_float(u.d[h][3]), sc.inv) & sc.keep;
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      o[h] = int8_pack4(bf16_lo_f32(u.d[0][2 * h]), bf16_hi_f32(u.d[0][2 * h]), bf16_lo_f32(u.d[0][2 * h + 1]),
-                        bf16_hi_f32(u.d[0][2 * h + 1]), sc.inv) & sc.keep;
-  }
-  return o;
-}
-
 // W waves per row; C units per thread held in registers.  Workgroups of max(W, 4) waves:
 // with W == 1 each of the four waves has a row of its own and nothing is synchronized.
 template <bool F32, bool STREAM, int W, int C>

@@ -619,7 +619,7 @@ mxq_status mxq_gemm_w8a8(const int8_t* a, int64_t ld_a, const float* a_scales, i
 }
 
 size_t mxq_gemm_w8a8_fused_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (!w8_shape_ok(M, N, K)) return 0;
+  if (!w8_shape_ok(M, N, K) || mxq::gemm_w8a8_one_launch(M, K)) return 0;
   return fused_codes_bytes(M, K) + mxq::gemm_w8a8_workspace_bytes(M, N, K);
 }
 
@@ -637,6 +637,9 @@ mxq_status mxq_gemm_w8a8_fused(const void* a, mxq_dtype dt, int64_t ld_a, const 
   if (need > 0 && (!workspace || !aligned(workspace, 16) || ws_bytes < need))
     return fail(MXQ_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned and hold %llu bytes", fn,
                 (unsigned long long)need);
+  if (need == 0)
+    return hip_status(fn, mxq::launch_gemm_w8a8_unquantized(a, dt == MXQ_F32, ld_a, w, ld_w, w_scales, inc_ws, bias, M, N,
+                                                            K, out, out_dt == MXQ_F32, ld_out, as_stream(stream)));
   int8_t* codes = static_cast<int8_t*>(workspace);
   float* scales = reinterpret_cast<float*>(codes + M * K);
   void* rest = mxq::gemm_w8a8_workspace_bytes(M, N, K) > 0 ? codes + fused_codes_bytes(M, K) : nullptr;

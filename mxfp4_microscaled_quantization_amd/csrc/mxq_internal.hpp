@@ -56,6 +56,12 @@ hipError_t launch_gemm_w8a8(const int8_t* a, int64_t ld_a, const float* a_scales
                             int64_t N, int64_t K, void* out, bool f32_out, int64_t ld_out, void* workspace,
                             hipStream_t stream);
 
+// The same from unquantized activations in one launch, where gemm_w8a8_one_launch (M, N > 0).
+bool gemm_w8a8_one_launch(int64_t M, int64_t K);
+hipError_t launch_gemm_w8a8_unquantized(const void* x, bool f32, int64_t ld_x, const int8_t* w, int64_t ld_w,
+                                        const float* w_scales, int64_t inc_ws, const float* bias, int64_t M, int64_t N,
+                                        int64_t K, void* out, bool f32_out, int64_t ld_out, hipStream_t stream);
+
 // Norm and rotation of query and key heads (qk_norm.hip).  Pitches in elements of the
 // tensor they belong to: ld_* between tokens, hs_* between heads.
 struct QkSide {

@@ -120,6 +120,11 @@ def test_workspace_covers_codes_and_scales():
         assert mxq.w8a8_fused_workspace_bytes(M, N, K) >= M * K + 4 * M
     for M, N, K in ((0, 8, 64), (8, 0, 64), (8, 8, 40), (-1, 8, 64), (8, 8, 1 << 17), (8, 8, -16)):
         assert mxq.w8a8_fused_workspace_bytes(M, N, K) == 0 and mxq.w8a8_workspace_bytes(M, N, K) == 0
+    # up to 8 tokens whose codes fit the LDS: one launch, no workspace
+    for M, N, K in ((1, 64, 15744), (8, 64, 1920), (3, 5120, 5248)):
+        assert mxq.w8a8_fused_workspace_bytes(M, N, K) == 0
+    for M, N, K in ((1, 64, 15760), (8, 64, 1936), (9, 64, 128)):
+        assert mxq.w8a8_fused_workspace_bytes(M, N, K) >= M * K + 4 * M
     assert mxq.w8a8_workspace_bytes(48, 5120, 13824) > 0 and mxq.w8a8_workspace_bytes(4096, 5120, 13824) == 0
     assert mxq.w8a8_fused_workspace_bytes(48, 5120, 13824) >= 48 * 13828 + mxq.w8a8_workspace_bytes(48, 5120, 13824)
 

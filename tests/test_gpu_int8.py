@@ -261,7 +261,10 @@ def test_product_scales_that_are_nan_or_zero_stay_in_their_row(gpu):
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("M,N,K", [(1, 64, 16), (1, 5120, 13824), (1, 13825, 5120), (2, 40, 1360), (3, 300, 2048),
                                    (4, 1000, 8192), (5, 129, 2064), (8, 77, 4112), (16, 512, 1024), (17, 96, 528),
-                                   (64, 256, 640), (100, 333, 1040), (300, 512, 784), (2, 33, 65552), (1, 9, 131056)])
+                                   (64, 256, 640), (100, 333, 1040), (300, 512, 784), (2, 33, 65552), (1, 9, 131056),
+                                   # the largest and the next K of the one-launch form, for 1, 2, 3 and 8 tokens
+                                   (1, 100, 15744), (1, 100, 15760), (2, 64, 7808), (2, 64, 7824), (3, 31, 5248), (3, 31, 5264), (8, 70, 1920),
+                                   (8, 70, 1936), (7, 50, 112), (6, 1000, 16), (8, 33, 144)])
 def test_fused_equals_the_two_calls(gpu, M, N, K, dtype):
     announce(f"gemm_w8a8_fused {M}x{N}x{K} {dtype}")
     x = _x(M, K, dtype, M + N + K, 2.0)
