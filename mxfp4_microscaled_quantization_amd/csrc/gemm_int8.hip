@@ -5,7 +5,7 @@
 //   out = v rounded to bf16 (nearest even), or v
 // The sum is exact in any order, so every kernel here gives the same bits.
 //
-// gemm_i8_kernel, one workgroup = WM x WN waves = a (16 MJ WM) x (16 MI WN) output tile,
+// i8_tile, one workgroup = WM x WN waves = a (16 MJ WM) x (16 MI WN) output tile,
 // 16 x 16 x 64 MFMAs:
 //  * the weight tile is the MFMA A operand and the activation tile the B operand, so a
 //    lane finishes with 4 consecutive output columns of one row.  Lane l holds row l & 15
@@ -42,6 +42,7 @@ struct I8Params {
   int nwin, tiles_m, tiles_n;
   int* part;               // int32 sums of the parts of K, [splits][M][ld_part]
   int splits, ld_part;
+  int whole;               // gemm_i8_tail_kernel: tiles in whole rounds
   int vec;                 // rows of the output start on 16-byte boundaries
   int vec_channels;        // channel scales and biases are contiguous and 16-byte aligned
 };
@@ -103,21 +104,23 @@ __device__ __forceinline__ float scaled(int acc, float sa, float sw, float bias,
   return has_bias ? __builtin_fmaf(t, sw, bias) : t * sw;
 }
 
-// Origin of this workgroup's tile.  Every XCD (workgroups are dealt to them in turn) walks
-// a contiguous run of tiles, kBand tiles high: 4 rows of tiles by 8 columns run at once on
-// its 32 CUs and share their operands in its L2 (2 % to 6 % faster than one row by 32 at
-// 75600 x 5120 x 13824 and 3584 x 5120 x 15360, and than 8 by 4 at long K).
+// Origin of tile `seq` of nt: bands of kBand rows of tiles, in which the index runs down the
+// rows first.  Every XCD (workgroups are dealt to them in turn) walks a contiguous run, so 4
+// rows of tiles by 8 columns run at once on its 32 CUs and share their operands in its L2
+// (2 % to 6 % faster than one row by 32 at 75600 x 5120 x 13824 and 3584 x 5120 x 15360, and
+// than 8 by 4 at long K).
 constexpr int kBand = 4;
 
-template <int BM, int BN>
-__device__ __forceinline__ void i8_tile_origin(const I8Params& p, int& m0, int& n0) {
-  const int nt = p.tiles_m * p.tiles_n, bid = blockIdx.x;
+__device__ __forceinline__ int xcd_run(int bid, int nt) {
   const int xcd = bid & 7, q8 = nt >> 3, r8 = nt & 7;
-  const int seq = xcd * q8 + min(xcd, r8) + (bid >> 3);
+  return xcd * q8 + min(xcd, r8) + (bid >> 3);
+}
+
+__device__ __forceinline__ void tile_at(const I8Params& p, int seq, int& tm, int& tn) {
   const int band = seq / (kBand * p.tiles_n), first = band * kBand, rows = min(kBand, p.tiles_m - first);
   const int in = seq - band * kBand * p.tiles_n;
-  m0 = (first + in % rows) * BM;
-  n0 = in / rows * BN;
+  tm = first + in % rows;
+  tn = in / rows;
 }
 
 // Scales and biases of 4 consecutive channels from n (clamped to the last one).
@@ -172,25 +175,34 @@ __device__ __forceinline__ void store_channels(const I8Params& p, int m, int n, 
 // of K (blockIdx.y of p.splits) for i8_reduce_kernel.
 enum { OUT_BF16 = 0, OUT_F32 = 1, OUT_PART = 2 };
 
-template <int MI, int MJ, int WM, int WN, int NA, int NW, int OUT>
-__global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(I8Params p) {
-  constexpr int WAVES = WM * WN, BM = 16 * MJ * WM, BN = 16 * MI * WN;
-  constexpr uint32_t A_TILE = BM * kWin, W_TILE = BN * kWin;
+template <int MI, int MJ, int WM, int WN, int NA, int NW>
+struct Tile {
+  static constexpr int WAVES = WM * WN, BM = 16 * MJ * WM, BN = 16 * MI * WN;
+  static constexpr uint32_t A_TILE = BM * kWin, W_TILE = BN * kWin, LDS = NA * A_TILE + NW * W_TILE;
+};
+using Tile256x256 = Tile<4, 8, 2, 4, 3, 2>;
+using Tile128x256 = Tile<4, 4, 2, 4, 3, 3>;
+using Tile128x128 = Tile<2, 4, 2, 4, 4, 4>;
+
+// One output tile from (m0, n0) by the whole workgroup, with LDS_BYTES of LDS.
+template <int OUT, uint32_t LDS_BYTES, int MI, int MJ, int WM, int WN, int NA, int NW>
+__device__ __forceinline__ void i8_tile(Tile<MI, MJ, WM, WN, NA, NW>, const I8Params& p, uint8_t* lds, int m0, int n0) {
+  using T = Tile<MI, MJ, WM, WN, NA, NW>;
+  constexpr int WAVES = T::WAVES, BM = T::BM, BN = T::BN;
+  constexpr uint32_t A_TILE = T::A_TILE, W_TILE = T::W_TILE;
   constexpr int LA = (int)(A_TILE / 1024) / WAVES, LW = (int)(W_TILE / 1024) / WAVES;   // 1 KB lines per wave
   constexpr int RD = MI + MJ, VM = LA + LW;
   static_assert(LA >= 1 && LW >= 1 && LA * WAVES * 1024 == (int)A_TILE && LW * WAVES * 1024 == (int)W_TILE, "whole lines");
   static_assert(NW >= 2 && (NA == NW || NA == NW + 1), "ring depths");
+  static_assert(T::LDS <= LDS_BYTES, "rings fit");
   // loads issued after the last piece of window w+1 when window w ends
   constexpr int IN_FLIGHT = (NW - 2) * VM + (NA > NW ? LA : 0);
   static_assert((NW - 1) * VM + (NA > NW ? LA : 0) < 64, "vmcnt range");
   constexpr uint32_t W_BASE = NA * A_TILE;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[NA * A_TILE + NW * W_TILE];
 
   const uint32_t tid = threadIdx.x, lane = tid & 63;
   const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(tid >> 6));
   const uint32_t wm = wave % WM, wn = wave / WM;
-  int m0, n0;
-  i8_tile_origin<BM, BN>(p, m0, n0);
   // this workgroup's windows of K
   const int w_lo = OUT == OUT_PART ? (int)((int64_t)blockIdx.y * p.nwin / p.splits) : 0;
   const int w_hi = OUT == OUT_PART ? (int)((int64_t)(blockIdx.y + 1) * p.nwin / p.splits) : p.nwin;
@@ -208,17 +220,21 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(I8Params p) {
   const uint32_t last_bytes = (uint32_t)(K - (nwin - 1) * kWin);   // of the last window: 16 .. 128
   // line j of this wave's share of window w, into ring slot `slot`; past the last window the
   // resource is empty, so that no memory is read and the loads in flight stay what the waits assume
+  const uint32_t va0 = drow * p.ld_a + chunk0, va1 = drow * p.ld_a + chunk1;
+  const uint32_t vw0 = drow * p.ld_w + chunk0, vw1 = drow * p.ld_w + chunk1;
+  const bool in0 = chunk0 < last_bytes, in1 = chunk1 < last_bytes;   // of the last window
   auto issue_a = [&](int w, uint32_t slot, int j) {
     const uint32_t line = wave * LA + j;
-    const uint32_t chunk = (line & 1) ? chunk1 : chunk0;
-    const uint32_t valid = w + 1 < nwin ? (uint32_t)kWin : last_bytes;
+    const bool odd = LA % 2 == 0 ? j & 1 : line & 1;
+    const bool in = w + 1 < nwin || (odd ? in1 : in0);
     line_to_lds(make_rsrc(base_a, w < nwin ? bytes_a : 0u), lds + slot * A_TILE + line * 1024,
-                chunk < valid ? drow * p.ld_a + chunk : kOutside, (uint32_t)w * kWin + line * 8 * p.ld_a);
+                in ? (odd ? va1 : va0) : kOutside, (uint32_t)w * kWin + line * 8 * p.ld_a);
   };
   auto issue_w = [&](int w, uint32_t slot, int j) {
     const uint32_t line = wave * LW + j;
+    const bool odd = LW % 2 == 0 ? j & 1 : line & 1;
     line_to_lds(make_rsrc(base_w, w < nwin ? bytes_w : 0u), lds + W_BASE + slot * W_TILE + line * 1024,
-                drow * p.ld_w + ((line & 1) ? chunk1 : chunk0), (uint32_t)w * kWin + line * 8 * p.ld_w);
+                odd ? vw1 : vw0, (uint32_t)w * kWin + line * 8 * p.ld_w);
   };
 
   v4i acc[MI][MJ];
@@ -229,19 +245,21 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(I8Params p) {
   v4i f0[RD], f1[RD];
   const uint32_t r16 = lane & 15, g = lane >> 4;
   // step-t fragments of the window in ring slots u mod NA, u mod NW: weight rows, then
-  // activation rows; after(k) follows read k
+  // activation rows; after(k) follows read k.  A lane reads chunk g + 4t of rows r16 + 16 i,
+  // whose swizzle is that of r16: one offset for t = 0, and the same with bit 6 turned for t = 1
+  const uint32_t frag = lds_slot(r16, g);
   auto read = [&](v4i(&f)[RD], uint32_t u, int t, auto&& after) {
-    const uint8_t* la = lds + u % NA * A_TILE;
-    const uint8_t* lw = lds + W_BASE + u % NW * W_TILE;
-    const uint32_t chunk = g + 4 * t;
+    const uint32_t at = frag ^ (64u * t);
+    const uint8_t* la = lds + (at + wm * (16 * MJ * 128) + u % NA * A_TILE);
+    const uint8_t* lw = lds + (at + wn * (16 * MI * 128) + W_BASE + u % NW * W_TILE);
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      f[i] = *reinterpret_cast<const v4i*>(lw + lds_slot(wn * (16 * MI) + 16 * i + r16, chunk));
+      f[i] = *reinterpret_cast<const v4i*>(lw + 2048 * i);
       after(i);
     }
 #pragma unroll
     for (int j = 0; j < MJ; ++j) {
-      f[MI + j] = *reinterpret_cast<const v4i*>(la + lds_slot(wm * (16 * MJ) + 16 * j + r16, chunk));
+      f[MI + j] = *reinterpret_cast<const v4i*>(la + 2048 * j);
       after(MI + j);
     }
   };
@@ -343,7 +361,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(I8Params p) {
       // whole row segments, past the caches: the tile is not read again here, and the
       // operands of the neighbouring tiles stay (about 1 %)
       static_assert((CPR & (CPR - 1)) == 0 && CPR <= 64, "a power of two");
-      static_assert(WAVES * 16 * MJ * RB <= sizeof(lds), "staging fits the rings");
+      static_assert(WAVES * 16 * MJ * RB <= LDS_BYTES, "staging fits the rings");
       __syncthreads();
       uint8_t* sub = lds + wave * (16 * MJ * RB);
 #pragma unroll
@@ -376,7 +394,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(I8Params p) {
   // elements where a row has no alignment: 1001 x 1360 x 2051 to binary32 took 17.2 us with
   // each lane storing its own columns, 14.8 here)
   constexpr int PITCH = 16 * MI + 4;               // floats per row in LDS
-  constexpr int FIT = (int)(sizeof(lds) / (WAVES * 16 * PITCH * 4));
+  constexpr int FIT = (int)(LDS_BYTES / (WAVES * 16 * PITCH * 4));
   constexpr int CJ = FIT >= MJ ? MJ : FIT >= 4 ? 4 : FIT >= 2 ? 2 : 1;
   static_assert(FIT >= 1 && MJ % CJ == 0, "whole passes");
   __syncthreads();
@@ -419,6 +437,39 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(I8Params p) {
         }
       }
     }
+  }
+}
+
+// Plain tiles, blockIdx.y the part of K.
+template <class T, int OUT>
+__global__ __launch_bounds__(64 * T::WAVES) void gemm_i8_kernel(I8Params p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
+  int tm, tn;
+  tile_at(p, xcd_run(blockIdx.x, p.tiles_m * p.tiles_n), tm, tn);
+  i8_tile<OUT, T::LDS>(T{}, p, lds, tm * T::BM, tn * T::BN);
+}
+
+// 256 x 256 tiles in whole rounds of the GPU (the first p.whole workgroups), and the tiles of
+// the last, partial round cut into PARTS smaller ones of type S, so that it keeps more of
+// the CUs busy.  Against whole tiles to the end: 3584 x 5120 x 5120 (280 tiles, 24 in the last
+// round, quarters) 110 -> 86 us, 4096 x 5120 x 5120 118 -> 91, 5000 x 2048 x 4096 58 -> 49,
+// 3584 x 5120 x 15360 238 -> 229; a last round of more than 128 tiles gains nothing.
+template <class S, int OUT>
+__global__ __launch_bounds__(512) void gemm_i8_tail_kernel(I8Params p) {
+  using T = Tile256x256;
+  constexpr int DOWN = T::BM / S::BM, PARTS = DOWN * (T::BN / S::BN);
+  static_assert(S::WAVES == T::WAVES, "one workgroup size");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
+  const int bid = blockIdx.x;
+  int tm, tn;
+  if (bid < p.whole) {
+    tile_at(p, xcd_run(bid, p.whole), tm, tn);
+    i8_tile<OUT, T::LDS>(T{}, p, lds, tm * T::BM, tn * T::BN);
+  } else {
+    const int part = (bid - p.whole) % PARTS;
+    tile_at(p, p.whole + (bid - p.whole) / PARTS, tm, tn);
+    const int m0 = tm * T::BM + part % DOWN * S::BM, n0 = tn * T::BN + part / DOWN * S::BN;
+    if (m0 < p.M && n0 < p.N) i8_tile<OUT, T::LDS>(S{}, p, lds, m0, n0);
   }
 }
 
@@ -479,7 +530,7 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_i8_few_kernel(I8Params p) {
   const int8_t* base_w = p.w + (int64_t)n0 * p.ld_w;
   const int nwin = p.nwin, start = (int)((int64_t)blockIdx.x * nwin / gridDim.x);
   const uint32_t last_bytes = (uint32_t)(p.K - (nwin - 1) * kWin);
-  const uint32_t drow = lane >> 3, dslot = lane & 7;   // as in gemm_i8_kernel
+  const uint32_t drow = lane >> 3, dslot = lane & 7;   // as in i8_tile
   const uint32_t chunk0 = (dslot ^ ((drow >> 1) & 7u)) * 16, chunk1 = (dslot ^ (((8u + drow) >> 1) & 7u)) * 16;
   uint8_t* ring = lds + (uint32_t)wave * (D * SLOT);
   auto window = [&](int w) { return w + start >= nwin ? w + start - nwin : w + start; };
@@ -635,12 +686,21 @@ constexpr TileCost kTileCost[TILES] = {
     {64, 128, 5.8f, 0.404f, 1.0f},   {128, 64, 5.8f, 0.404f, 1.0f},   {64, 64, 4.2f, 0.288f, 0.75f},
     {64, 32, 4.0f, 0.222f, 0.75f},   {32, 64, 4.0f, 0.225f, 0.75f},   {32, 32, 3.2f, 0.162f, 0.75f}};
 struct Plan {
-  int tile, splits;
+  int tile, splits, tail;   // tail: the tile that the last round of 256 x 256 tiles is cut into, or -1
 };
 Plan plan_w8a8(int64_t M, int64_t N, int64_t K, bool may_split) {
   const int64_t nwin = (K + kWin - 1) / kWin;
-  Plan best{TILE_256x256, 1};
+  Plan best{TILE_256x256, 1, -1};
   double least = 0;
+  auto consider = [&](double us, Plan plan) {
+    if (least == 0 || us < least) {
+      least = us;
+      best = plan;
+    }
+  };
+  auto round = [&](int t, int64_t windows) {
+    return kTileCost[t].fixed - kLaunch + kTileCost[t].per_window * (double)windows;
+  };
   for (int t = 0; t < TILES; ++t) {
     const TileCost& c = kTileCost[t];
     const int64_t tiles = ((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
@@ -648,13 +708,15 @@ Plan plan_w8a8(int64_t M, int64_t N, int64_t K, bool may_split) {
     for (int s = 1; s <= (may_split ? 8 : 1); ++s) {
       if (s > 1 && (tiles * s > 256 || nwin < 8 * s)) break;
       const double further = (double)((tiles * s + 255) / 256 - 1);
-      double us = kLaunch + (c.fixed - kLaunch + c.per_window * (double)((nwin + s - 1) / s)) * (1.0 + c.again * further);
+      double us = kLaunch + round(t, (nwin + s - 1) / s) * (1.0 + c.again * further);
       if (s > 1) us += 4.5 + (double)s * (double)M * (double)N * 8.0 / 5e6;
-      if (least == 0 || us < least) {
-        least = us;
-        best = {t, s};
-      }
+      consider(us, {t, s, -1});
     }
+    const int64_t rest = tiles % 256;
+    if (t == TILE_256x256 && tiles > 256 && rest > 0 && rest <= 128)
+      for (int tail = TILE_128x256; tail <= TILE_128x128; ++tail)
+        if (rest * (tail == TILE_128x256 ? 2 : 4) <= 256)
+          consider(kLaunch + round(t, nwin) * (double)(tiles / 256) + round(tail, nwin), {t, 1, tail});
   }
   return best;
 }
@@ -734,23 +796,38 @@ hipError_t launch_gemm_w8a8(const int8_t* a, int64_t ld_a, const float* a_scales
   }
   const Plan plan = plan_w8a8(M, N, K, workspace != nullptr);
   p.splits = plan.splits;
-  auto tile = [&](auto kernel, int bm, int bn, int waves) {
-    p.tiles_m = (int)((M + bm - 1) / bm);
-    p.tiles_n = (int)((N + bn - 1) / bn);
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(p.tiles_m * p.tiles_n), (unsigned)p.splits), dim3(64 * waves), 0, stream, p);
+  auto tile = [&](auto tile_tag, auto o_tag) {
+    using T = decltype(tile_tag);
+    p.tiles_m = (int)((M + T::BM - 1) / T::BM);
+    p.tiles_n = (int)((N + T::BN - 1) / T::BN);
+    hipLaunchKernelGGL((gemm_i8_kernel<T, decltype(o_tag)::value>), dim3((unsigned)(p.tiles_m * p.tiles_n), (unsigned)p.splits),
+                       dim3(64 * T::WAVES), 0, stream, p);
+  };
+  auto with_tail = [&](auto small_tag, auto o_tag) {
+    using T = Tile256x256;
+    using S = decltype(small_tag);
+    p.tiles_m = (int)((M + T::BM - 1) / T::BM);
+    p.tiles_n = (int)((N + T::BN - 1) / T::BN);
+    const int tiles = p.tiles_m * p.tiles_n, parts = (T::BM / S::BM) * (T::BN / S::BN);
+    p.whole = tiles / 256 * 256;
+    hipLaunchKernelGGL((gemm_i8_tail_kernel<S, decltype(o_tag)::value>), dim3((unsigned)(p.whole + (tiles - p.whole) * parts)),
+                       dim3(64 * T::WAVES), 0, stream, p);
   };
   auto pick = [&](auto o_tag) {
-    constexpr int O = decltype(o_tag)::value;
+    if constexpr (decltype(o_tag)::value != OUT_PART) {
+      if (plan.tail == TILE_128x256) return with_tail(Tile128x256{}, o_tag);
+      if (plan.tail == TILE_128x128) return with_tail(Tile128x128{}, o_tag);
+    }
     switch (plan.tile) {
-      case TILE_256x256: tile(gemm_i8_kernel<4, 8, 2, 4, 3, 2, O>, 256, 256, 8); break;
-      case TILE_128x256: tile(gemm_i8_kernel<4, 4, 2, 4, 3, 3, O>, 128, 256, 8); break;
-      case TILE_128x128: tile(gemm_i8_kernel<2, 4, 2, 4, 4, 4, O>, 128, 128, 8); break;
-      case TILE_64x128: tile(gemm_i8_kernel<2, 2, 2, 4, 6, 6, O>, 64, 128, 8); break;
-      case TILE_128x64: tile(gemm_i8_kernel<2, 4, 2, 2, 6, 6, O>, 128, 64, 4); break;
-      case TILE_64x64: tile(gemm_i8_kernel<2, 2, 2, 2, 4, 4, O>, 64, 64, 4); break;
-      case TILE_64x32: tile(gemm_i8_kernel<1, 2, 2, 2, 6, 6, O>, 64, 32, 4); break;
-      case TILE_32x64: tile(gemm_i8_kernel<2, 1, 2, 2, 6, 6, O>, 32, 64, 4); break;
-      default: tile(gemm_i8_kernel<1, 1, 2, 2, 8, 8, O>, 32, 32, 4); break;
+      case TILE_256x256: return tile(Tile256x256{}, o_tag);
+      case TILE_128x256: return tile(Tile128x256{}, o_tag);
+      case TILE_128x128: return tile(Tile128x128{}, o_tag);
+      case TILE_64x128: return tile(Tile<2, 2, 2, 4, 6, 6>{}, o_tag);
+      case TILE_128x64: return tile(Tile<2, 4, 2, 2, 6, 6>{}, o_tag);
+      case TILE_64x64: return tile(Tile<2, 2, 2, 2, 4, 4>{}, o_tag);
+      case TILE_64x32: return tile(Tile<1, 2, 2, 2, 6, 6>{}, o_tag);
+      case TILE_32x64: return tile(Tile<2, 1, 2, 2, 6, 6>{}, o_tag);
+      default: return tile(Tile<1, 1, 2, 2, 8, 8>{}, o_tag);
     }
   };
   if (p.splits > 1) {

@@ -170,7 +170,9 @@ SHAPES = [(1, 1, 16), (1, 5120, 1360), (2, 3, 131056), (1, 17, 4096), (3, 16, 64
           # every tile, and splits of K with a ragged last part
           (9, 5120, 96), (30, 13824, 160), (48, 5120, 13824), (60, 515, 13808), (60, 7000, 304), (130, 5120, 1040), (250, 13824, 272),
           (256, 5120, 8192), (500, 5120, 400), (500, 770, 16000), (700, 13824, 144), (1300, 5120, 272), (2100, 5000, 160),
-          (64, 256, 131056)]
+          (64, 256, 131056),
+          # a last round of the largest tile cut into halves and quarters, ragged at both edges
+          (4100, 4500, 48), (3900, 4700, 1040), (4400, 5000, 400), (4099, 4501, 160)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
