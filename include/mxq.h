@@ -344,6 +344,7 @@ mxq_status mxq_dequantize_int8(const int8_t* codes, int64_t ld_codes, const floa
  *     one scale for all).  bias : float[N] or NULL.
  * out : M x N of out_dt, pitch ld_out elements (>= N), naturally aligned.
  * K % 16 == 0 and K < 2^17 (the sum then fits int32); K == 0 gives the bias, or zeros.
+ * N <= 2^28, and M x N covered by at most 2^22 tiles of 256 x 256.
  * workspace, ws_bytes : NULL (0), or device memory of at least
  *     mxq_gemm_w8a8_workspace_bytes(M, N, K) bytes, 16-byte aligned, owned by the caller and
  *     not used by anything else until the call's work on `stream` is done.  With one, a

@@ -551,7 +551,8 @@ def _w8_out(M, N, device, out, out_dtype):
 def gemm_w8a8(a_codes, a_scales, w_codes, w_scales, bias=None, out=None, out_dtype=torch.bfloat16):
     """8-bit A [M, K] x W [N, K]^T with a scale for each token and channel -> bf16 or fp32 [M, N]:
     (sum in int32) * a_scales[m] * w_scales[n] + bias[n].  Rows may be strided, scales too (or expanded from one
-    value); ``out`` decides the output type where it is given."""
+    value), ``bias`` is float32; ``out`` decides the output type where it is given.  Like every entry point here it
+    records nothing for autograd."""
     lda = _matrix(a_codes, "a_codes", torch.int8)
     dev = a_codes.device
     M, K = a_codes.shape
@@ -677,7 +678,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions=None, eps=1e-6, s
     [P, R / 2], R <= D the rotated width, or None for the norm alone.  ``positions``: int64 [T], rows of the tables
     (token t has row t if None); a position outside the tables gives NaN.  ``style``: the pairs that turn,
     "interleaved" (2i, 2i+1) or "halves" (i, i + R/2).  Returns (q, k) of the input's type; ``out_q=q`` and
-    ``out_k=k`` work in place."""
+    ``out_k=k`` work in place.  Like every entry point here it records nothing for autograd."""
     args = _qk_inputs(q, k, q_weight, k_weight, cos, sin, positions, eps, style)
     out_q, (ldq, hsq) = _head_out(q, out_q, "out_q")
     out_k, (ldk, hsk) = _head_out(k, out_k, "out_k")

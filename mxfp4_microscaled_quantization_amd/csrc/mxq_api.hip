@@ -117,7 +117,9 @@ mxq_status check_w8(const char* fn, const int8_t* w, int64_t ld_w, const float* 
     return fail(MXQ_ERR_INVALID_ARG, "%s: ld_w (%lld) must be at least K and below 2^23", fn, (long long)ld_w);
   if (inc_ws < 0 || !pitch_ok(inc_ws)) return fail(MXQ_ERR_INVALID_ARG, "%s: inc_ws out of range", fn);
   if (M > 0 && N > 0) {
-    if (((M + 255) / 256) * ((N + 255) / 256) > ((int64_t)1 << 22))   // threads of a launch stay below 2^32
+    // threads of a launch stay below 2^32: 512 for each 256 x 256 tile, 256 for each 32 channels
+    // of a few tokens
+    if (((M + 255) / 256) * ((N + 255) / 256) > ((int64_t)1 << 22) || N > ((int64_t)1 << 28))
       return fail(MXQ_ERR_INVALID_ARG, "%s: problem too large", fn);
     if (!out) return fail(MXQ_ERR_INVALID_ARG, "%s: out is NULL", fn);
     if (!aligned(out, (uintptr_t)ob)) return fail(MXQ_ERR_INVALID_ARG, "%s: out must be %d-byte aligned", fn, ob);

@@ -68,6 +68,7 @@ INVALID = [
     (_gemm, dict(bias=ODD2), "bias"), (_gemm, dict(out=None), "out is NULL"), (_gemm, dict(out=P(0x10001)), "2-byte"),
     (_gemm, dict(out=ODD2, dt=0), "4-byte"), (_gemm, dict(ldo=7), "ld_out"), (_gemm, dict(ldo=BIG), "ld_out"),
     (_gemm, dict(M=2 ** 30, N=2 ** 20, ldo=2 ** 20), "too large"),
+    (_gemm, dict(M=1, N=2 ** 28 + 1, ldo=2 ** 29), "too large"), (_fused, dict(M=8, N=2 ** 29, ldo=2 ** 29), "too large"),
     (_gemm, dict(ws=ODD8, nbytes=1 << 30), "workspace"),
     (_gemm, dict(M=48, N=5120, K=13824, lda=13824, ldw=13824, ldo=5120, ws=OK16, nbytes=16), "workspace"),
     (_fused, dict(K=56, lda=56), "multiple of 16"), (_fused, dict(lda=48), "ld_x"), (_fused, dict(lda=68), "aligned"),
