@@ -669,7 +669,8 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_i8_few_kernel(I8Params p) {
 // Choice of the tile, and of a split of K.  Every kernel gives the same sums, so this is
 // about time alone.  A round of up to 256 tiles (one for each CU) takes fixed + per_window
 // * windows us with the tile in question, kLaunch of it once; a further round takes `again`
-// of the first (less than 1 where two workgroups fit a CU); a split of K adds the reduction
+// of the first (less than 1 where two workgroups fit a CU), or what dispatching 256 workgroups
+// takes (4052 x 80 x 1491: 64 x 64 tiles 13.3 us, 32 x 32 28); a split of K adds the reduction
 // and its traffic.  The constants are fits to times with cold operands, K = 5120 and 13824.
 // So a small tile is taken until a larger one fills the CUs, and the largest past that:
 //   512 x 5120 x 5120: 256 x 256 58 us, 128 x 256 40, 128 x 128 28, 64 x 128 40, 64 x 64 34
@@ -679,7 +680,7 @@ struct TileCost {
   int bm, bn;
   float fixed, per_window, again;
 };
-constexpr float kLaunch = 3.0f;
+constexpr float kLaunch = 3.0f, kDispatch = 1.07f;
 enum { TILE_256x256, TILE_128x256, TILE_128x128, TILE_64x128, TILE_128x64, TILE_64x64, TILE_64x32, TILE_32x64, TILE_32x32, TILES };
 constexpr TileCost kTileCost[TILES] = {
     {256, 256, 12.2f, 1.156f, 1.0f}, {128, 256, 11.7f, 0.728f, 1.0f}, {128, 128, 6.5f, 0.537f, 1.0f},
@@ -708,7 +709,8 @@ Plan plan_w8a8(int64_t M, int64_t N, int64_t K, bool may_split) {
     for (int s = 1; s <= (may_split ? 8 : 1); ++s) {
       if (s > 1 && (tiles * s > 256 || nwin < 8 * s)) break;
       const double further = (double)((tiles * s + 255) / 256 - 1);
-      double us = kLaunch + round(t, (nwin + s - 1) / s) * (1.0 + c.again * further);
+      const double first = round(t, (nwin + s - 1) / s);
+      double us = kLaunch + first + (c.again * first > kDispatch ? c.again * first : kDispatch) * further;
       if (s > 1) us += 4.5 + (double)s * (double)M * (double)N * 8.0 / 5e6;
       consider(us, {t, s, -1});
     }

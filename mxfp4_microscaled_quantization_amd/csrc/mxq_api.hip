@@ -140,8 +140,11 @@ bool w8_shape_ok(int64_t M, int64_t N, int64_t K) {
   return M > 0 && N > 0 && K >= 0 && K % 16 == 0 && M <= kMaxDim - 256 && N <= kMaxDim - 256 && K < ((int64_t)1 << 17);
 }
 
-// Codes and scales of quantized activations, in 16-byte steps.
-size_t fused_codes_bytes(int64_t M, int64_t K) { return (size_t)M * (size_t)K + ((size_t)M + 3) / 4 * 16; }
+// Codes and scales of quantized activations, in 16-byte steps.  Rows of codes start on cache
+// lines (128 bytes), which the product reads faster than others (1144 x 4272 x 384: 18.8 ->
+// 16.9 us, 3000 x 5008 x 5120: 87 -> 82).
+int64_t fused_pitch(int64_t K) { return (K + 127) / 128 * 128; }
+size_t fused_codes_bytes(int64_t M, int64_t K) { return (size_t)M * (size_t)fused_pitch(K) + ((size_t)M + 3) / 4 * 16; }
 
 // Arguments of one side (queries or keys) of the head norm.
 struct HeadArgs {
@@ -643,11 +646,12 @@ mxq_status mxq_gemm_w8a8_fused(const void* a, mxq_dtype dt, int64_t ld_a, const 
     return hip_status(fn, mxq::launch_gemm_w8a8_unquantized(a, dt == MXQ_F32, ld_a, w, ld_w, w_scales, inc_ws, bias, M, N,
                                                             K, out, out_dt == MXQ_F32, ld_out, as_stream(stream)));
   int8_t* codes = static_cast<int8_t*>(workspace);
-  float* scales = reinterpret_cast<float*>(codes + M * K);
+  const int64_t pitch = fused_pitch(K);
+  float* scales = reinterpret_cast<float*>(codes + M * pitch);
   void* rest = mxq::gemm_w8a8_workspace_bytes(M, N, K) > 0 ? codes + fused_codes_bytes(M, K) : nullptr;
-  hipError_t e = mxq::launch_quantize_int8(a, dt == MXQ_F32, M, K, ld_a, codes, K, scales, as_stream(stream));
+  hipError_t e = mxq::launch_quantize_int8(a, dt == MXQ_F32, M, K, ld_a, codes, pitch, scales, as_stream(stream));
   if (e == hipSuccess)
-    e = mxq::launch_gemm_w8a8(codes, K, scales, 1, w, ld_w, w_scales, inc_ws, bias, M, N, K, out, out_dt == MXQ_F32,
+    e = mxq::launch_gemm_w8a8(codes, pitch, scales, 1, w, ld_w, w_scales, inc_ws, bias, M, N, K, out, out_dt == MXQ_F32,
                               ld_out, rest, as_stream(stream));
   return hip_status(fn, e);
 }
