@@ -18,6 +18,11 @@
 //  * ragged M and N: rows past the end are outside the buffer resource and read as zeros.
 //    Ragged K: in the last window the activation chunks past K are fetched from outside
 //    the resource, i.e. as zeros, which cancel whatever the weight row holds there.
+//  * rows that do not start on a cache line (128 bytes): a window of such a row takes three
+//    half lines instead of two, and the path of the loads into LDS is what bounds the smaller
+//    tiles.  Their SHIFT form loads whole lines, block w of a row being its line w, and a
+//    fragment read takes its chunk from block w or w + 1, which the ring holds both (pitches
+//    are multiples of 16, so that a row's offset in its line is the same every 8 rows).
 #include <type_traits>
 #include <utility>
 
@@ -175,7 +180,8 @@ __device__ __forceinline__ void store_channels(const I8Params& p, int m, int n, 
 // of K (blockIdx.y of p.splits) for i8_reduce_kernel.
 enum { OUT_BF16 = 0, OUT_F32 = 1, OUT_PART = 2 };
 
-template <int MI, int MJ, int WM, int WN, int NA, int NW>
+// SHIFT: for operands whose rows do not all start on a cache line (128 bytes).
+template <int MI, int MJ, int WM, int WN, int NA, int NW, bool SHIFT = false>
 struct Tile {
   static constexpr int WAVES = WM * WN, BM = 16 * MJ * WM, BN = 16 * MI * WN;
   static constexpr uint32_t A_TILE = BM * kWin, W_TILE = BN * kWin, LDS = NA * A_TILE + NW * W_TILE;
@@ -184,19 +190,27 @@ using Tile256x256 = Tile<4, 8, 2, 4, 3, 2>;
 using Tile128x256 = Tile<4, 4, 2, 4, 3, 3>;
 using Tile128x128 = Tile<2, 4, 2, 4, 4, 4>;
 
+// The same tile for rows off the cache lines: the rings need a third weight block.
+template <class T> struct Shift;
+template <int MI, int MJ, int WM, int WN, int NA, int NW>
+struct Shift<Tile<MI, MJ, WM, WN, NA, NW>> { using type = Tile<MI, MJ, WM, WN, NW == 3 ? 4 : NA, NW, NW >= 3>; };
+template <class T> using Shifted = typename Shift<T>::type;
+
 // One output tile from (m0, n0) by the whole workgroup, with LDS_BYTES of LDS.
-template <int OUT, uint32_t LDS_BYTES, int MI, int MJ, int WM, int WN, int NA, int NW>
-__device__ __forceinline__ void i8_tile(Tile<MI, MJ, WM, WN, NA, NW>, const I8Params& p, uint8_t* lds, int m0, int n0) {
-  using T = Tile<MI, MJ, WM, WN, NA, NW>;
+template <int OUT, uint32_t LDS_BYTES, int MI, int MJ, int WM, int WN, int NA, int NW, bool SHIFT>
+__device__ __forceinline__ void i8_tile(Tile<MI, MJ, WM, WN, NA, NW, SHIFT>, const I8Params& p, uint8_t* lds, int m0, int n0) {
+  using T = Tile<MI, MJ, WM, WN, NA, NW, SHIFT>;
   constexpr int WAVES = T::WAVES, BM = T::BM, BN = T::BN;
   constexpr uint32_t A_TILE = T::A_TILE, W_TILE = T::W_TILE;
   constexpr int LA = (int)(A_TILE / 1024) / WAVES, LW = (int)(W_TILE / 1024) / WAVES;   // 1 KB lines per wave
   constexpr int RD = MI + MJ, VM = LA + LW;
   static_assert(LA >= 1 && LW >= 1 && LA * WAVES * 1024 == (int)A_TILE && LW * WAVES * 1024 == (int)W_TILE, "whole lines");
-  static_assert(NW >= 2 && (NA == NW || NA == NW + 1), "ring depths");
+  static_assert(NW >= 2 && (NA == NW || NA == NW + 1) && (!SHIFT || NA + NW >= 7), "ring depths");
   static_assert(T::LDS <= LDS_BYTES, "rings fit");
-  // loads issued after the last piece of window w+1 when window w ends
-  constexpr int IN_FLIGHT = (NW - 2) * VM + (NA > NW ? LA : 0);
+  // a window's reads reach AHEAD further blocks; the loads issued after the last piece of block
+  // w+1+AHEAD when window w ends
+  constexpr int AHEAD = SHIFT ? 1 : 0;
+  constexpr int IN_FLIGHT = (NW - 2 - AHEAD) * VM + (NA > NW ? LA : 0);
   static_assert((NW - 1) * VM + (NA > NW ? LA : 0) < 64, "vmcnt range");
   constexpr uint32_t W_BASE = NA * A_TILE;
 
@@ -208,9 +222,13 @@ __device__ __forceinline__ void i8_tile(Tile<MI, MJ, WM, WN, NA, NW>, const I8Pa
   const int w_hi = OUT == OUT_PART ? (int)((int64_t)(blockIdx.y + 1) * p.nwin / p.splits) : p.nwin;
   const int nwin = w_hi - w_lo, K = min(p.K, w_hi * kWin) - w_lo * kWin;
   const uint32_t rows_a = (uint32_t)min(BM, p.M - m0), rows_w = (uint32_t)min(BN, p.N - n0);
-  const uint32_t bytes_a = (rows_a - 1) * p.ld_a + (uint32_t)K, bytes_w = (rows_w - 1) * p.ld_w + (uint32_t)K;
   const int8_t* base_a = p.a + (int64_t)m0 * p.ld_a + w_lo * kWin;
   const int8_t* base_w = p.w + (int64_t)n0 * p.ld_w + w_lo * kWin;
+  // SHIFT: the resources start at the cache line of their first row
+  const uint32_t off_a = SHIFT ? (uint32_t)(uintptr_t)base_a & 127u : 0u, off_w = SHIFT ? (uint32_t)(uintptr_t)base_w & 127u : 0u;
+  base_a -= off_a;
+  base_w -= off_w;
+  const uint32_t bytes_a = off_a + (rows_a - 1) * p.ld_a + (uint32_t)K, bytes_w = off_w + (rows_w - 1) * p.ld_w + (uint32_t)K;
 
   // direct-to-LDS lines: LDS line q holds rows 8q .. 8q+7; lane i lands at byte 16 i, in
   // row i / 8 at slot i % 8, and fetches the chunk the swizzle maps there (whose term
@@ -220,21 +238,26 @@ __device__ __forceinline__ void i8_tile(Tile<MI, MJ, WM, WN, NA, NW>, const I8Pa
   const uint32_t last_bytes = (uint32_t)(K - (nwin - 1) * kWin);   // of the last window: 16 .. 128
   // line j of this wave's share of window w, into ring slot `slot`; past the last window the
   // resource is empty, so that no memory is read and the loads in flight stay what the waits assume
-  const uint32_t va0 = drow * p.ld_a + chunk0, va1 = drow * p.ld_a + chunk1;
-  const uint32_t vw0 = drow * p.ld_w + chunk0, vw1 = drow * p.ld_w + chunk1;
+  // SHIFT: block w of a row is its cache line w, which starts `ph` bytes before window w; ph is
+  // the same every 8 rows, since pitches are multiples of 16
+  const uint32_t ph_a = (off_a + (SHIFT ? drow * p.ld_a : 0u)) & 127u, ph_w = (off_w + (SHIFT ? drow * p.ld_w : 0u)) & 127u;
+  const uint32_t row_a = drow * p.ld_a + off_a - ph_a, row_w = drow * p.ld_w + off_w - ph_w;
+  const uint32_t va0 = row_a + chunk0, va1 = row_a + chunk1, vw0 = row_w + chunk0, vw1 = row_w + chunk1;
   const bool in0 = chunk0 < last_bytes, in1 = chunk1 < last_bytes;   // of the last window
   auto issue_a = [&](int w, uint32_t slot, int j) {
     const uint32_t line = wave * LA + j;
     const bool odd = LA % 2 == 0 ? j & 1 : line & 1;
-    const bool in = w + 1 < nwin || (odd ? in1 : in0);
-    line_to_lds(make_rsrc(base_a, w < nwin ? bytes_a : 0u), lds + slot * A_TILE + line * 1024,
+    const bool in = SHIFT ? (uint32_t)w * kWin + (odd ? chunk1 : chunk0) - ph_a < (uint32_t)K
+                          : w + 1 < nwin || (odd ? in1 : in0);
+    line_to_lds(make_rsrc(base_a, SHIFT || w < nwin ? bytes_a : 0u), lds + slot * A_TILE + line * 1024,
                 in ? (odd ? va1 : va0) : kOutside, (uint32_t)w * kWin + line * 8 * p.ld_a);
   };
   auto issue_w = [&](int w, uint32_t slot, int j) {
     const uint32_t line = wave * LW + j;
     const bool odd = LW % 2 == 0 ? j & 1 : line & 1;
-    line_to_lds(make_rsrc(base_w, w < nwin ? bytes_w : 0u), lds + W_BASE + slot * W_TILE + line * 1024,
-                odd ? vw1 : vw0, (uint32_t)w * kWin + line * 8 * p.ld_w);
+    const bool in = !SHIFT || (uint32_t)w * kWin + (odd ? chunk1 : chunk0) - ph_w < (uint32_t)K;
+    line_to_lds(make_rsrc(base_w, SHIFT || w < nwin ? bytes_w : 0u), lds + W_BASE + slot * W_TILE + line * 1024,
+                in ? (odd ? vw1 : vw0) : kOutside, (uint32_t)w * kWin + line * 8 * p.ld_w);
   };
 
   v4i acc[MI][MJ];
@@ -247,11 +270,14 @@ __device__ __forceinline__ void i8_tile(Tile<MI, MJ, WM, WN, NA, NW>, const I8Pa
   // step-t fragments of the window in ring slots u mod NA, u mod NW: weight rows, then
   // activation rows; after(k) follows read k.  A lane reads chunk g + 4t of rows r16 + 16 i,
   // whose swizzle is that of r16: one offset for t = 0, and the same with bit 6 turned for t = 1
-  const uint32_t frag = lds_slot(r16, g);
+  // SHIFT: the chunks of a row are counted from its block, and those past 7 are in the next
+  const uint32_t ca = g + (((off_a + r16 * p.ld_a) & 127u) >> 4), cw = g + (((off_w + r16 * p.ld_w) & 127u) >> 4);
+  const uint32_t frag_a = lds_slot(r16, SHIFT ? ca & 7u : g) + wm * (16 * MJ * 128);
+  const uint32_t frag_w = lds_slot(r16, SHIFT ? cw & 7u : g) + wn * (16 * MI * 128) + W_BASE;
   auto read = [&](v4i(&f)[RD], uint32_t u, int t, auto&& after) {
-    const uint32_t at = frag ^ (64u * t);
-    const uint8_t* la = lds + (at + wm * (16 * MJ * 128) + u % NA * A_TILE);
-    const uint8_t* lw = lds + (at + wn * (16 * MI * 128) + W_BASE + u % NW * W_TILE);
+    const bool over_a = SHIFT && ca + 4 * t > 7, over_w = SHIFT && cw + 4 * t > 7;
+    const uint8_t* la = lds + ((frag_a ^ (64u * t)) + (over_a ? (u + 1) % NA : u % NA) * A_TILE);
+    const uint8_t* lw = lds + ((frag_w ^ (64u * t)) + (over_w ? (u + 1) % NW : u % NW) * W_TILE);
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       f[i] = *reinterpret_cast<const v4i*>(lw + 2048 * i);
@@ -325,7 +351,7 @@ __device__ __forceinline__ void i8_tile(Tile<MI, MJ, WM, WN, NA, NW>, const I8Pa
 #pragma unroll
       for (int j = 0; j < LA; ++j) issue_a(w + NA - NW, w + NA - NW, j);
     }
-    __builtin_amdgcn_s_waitcnt(wait_vm((NW - 1) * VM + (NA > NW ? LA : 0)));   // window 0 landed
+    __builtin_amdgcn_s_waitcnt(wait_vm((NW - 1 - AHEAD) * VM + (NA > NW ? LA : 0)));   // window 0 landed
     handover_barrier();
     read(f0, 0, 0, [](int) {});
     for (int w = 0; turn(w); w += TURN) {
@@ -676,16 +702,18 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_i8_few_kernel(I8Params p) {
 //   512 x 5120 x 5120: 256 x 256 58 us, 128 x 256 40, 128 x 128 28, 64 x 128 40, 64 x 64 34
 //   2048 x 5120 x 5120: 57, 78, 79, 99, 102;  128 x 5120 x 5120: 60, 43, 29, 22, 15.5
 //   64 x 13824 x 5120: 64 x 32 27.5, 64 x 64 36, 64 x 64 in 3 parts of K 20.6
+// off_lines: factor on per_window where K is no multiple of a cache line, so that contiguous rows
+// start off the lines.
 struct TileCost {
   int bm, bn;
-  float fixed, per_window, again;
+  float fixed, per_window, again, off_lines;
 };
 constexpr float kLaunch = 3.0f, kDispatch = 1.07f;
 enum { TILE_256x256, TILE_128x256, TILE_128x128, TILE_64x128, TILE_128x64, TILE_64x64, TILE_64x32, TILE_32x64, TILE_32x32, TILES };
 constexpr TileCost kTileCost[TILES] = {
-    {256, 256, 12.2f, 1.156f, 1.0f}, {128, 256, 11.7f, 0.728f, 1.0f}, {128, 128, 6.5f, 0.537f, 1.0f},
-    {64, 128, 5.8f, 0.404f, 1.0f},   {128, 64, 5.8f, 0.404f, 1.0f},   {64, 64, 4.2f, 0.288f, 0.75f},
-    {64, 32, 4.0f, 0.222f, 0.75f},   {32, 64, 4.0f, 0.225f, 0.75f},   {32, 32, 3.2f, 0.162f, 0.75f}};
+    {256, 256, 12.2f, 1.156f, 1.0f, 1.3f},  {128, 256, 11.7f, 0.728f, 1.0f, 1.25f}, {128, 128, 6.5f, 0.537f, 1.0f, 1.06f},
+    {64, 128, 5.8f, 0.404f, 1.0f, 1.06f},   {128, 64, 5.8f, 0.404f, 1.0f, 1.06f},   {64, 64, 4.2f, 0.288f, 0.75f, 1.06f},
+    {64, 32, 4.0f, 0.222f, 0.75f, 1.06f},   {32, 64, 4.0f, 0.225f, 0.75f, 1.06f},   {32, 32, 3.2f, 0.162f, 0.75f, 1.06f}};
 struct Plan {
   int tile, splits, tail;   // tail: the tile that the last round of 256 x 256 tiles is cut into, or -1
 };
@@ -700,7 +728,8 @@ Plan plan_w8a8(int64_t M, int64_t N, int64_t K, bool may_split) {
     }
   };
   auto round = [&](int t, int64_t windows) {
-    return kTileCost[t].fixed - kLaunch + kTileCost[t].per_window * (double)windows;
+    const TileCost& c = kTileCost[t];
+    return c.fixed - kLaunch + (K % kWin ? c.off_lines : 1.0f) * c.per_window * (double)windows;
   };
   for (int t = 0; t < TILES; ++t) {
     const TileCost& c = kTileCost[t];
@@ -798,12 +827,21 @@ hipError_t launch_gemm_w8a8(const int8_t* a, int64_t ld_a, const float* a_scales
   }
   const Plan plan = plan_w8a8(M, N, K, workspace != nullptr);
   p.splits = plan.splits;
+  auto on_lines = [](const int8_t* q, int64_t ld) { return ((uintptr_t)q | (uintptr_t)ld) % 128 == 0; };
+  // For K up to 1024 the plain tiles are as fast off the lines (700 x 400 x 2000: 6.3 us, shifted
+  // 6.5; 1001 x 1360 x 2051: 12.0 and 11.4, 1024 x 4112 x 4096: 32 and 23.5).
+  const bool shift = p.nwin > 8 && !(on_lines(a, ld_a) && on_lines(w, ld_w));
   auto tile = [&](auto tile_tag, auto o_tag) {
     using T = decltype(tile_tag);
     p.tiles_m = (int)((M + T::BM - 1) / T::BM);
     p.tiles_n = (int)((N + T::BN - 1) / T::BN);
-    hipLaunchKernelGGL((gemm_i8_kernel<T, decltype(o_tag)::value>), dim3((unsigned)(p.tiles_m * p.tiles_n), (unsigned)p.splits),
-                       dim3(64 * T::WAVES), 0, stream, p);
+    auto go = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)(p.tiles_m * p.tiles_n), (unsigned)p.splits), dim3(64 * T::WAVES), 0, stream, p);
+    };
+    if (shift)
+      go(gemm_i8_kernel<Shifted<T>, decltype(o_tag)::value>);
+    else
+      go(gemm_i8_kernel<T, decltype(o_tag)::value>);
   };
   auto with_tail = [&](auto small_tag, auto o_tag) {
     using T = Tile256x256;
@@ -812,8 +850,13 @@ hipError_t launch_gemm_w8a8(const int8_t* a, int64_t ld_a, const float* a_scales
     p.tiles_n = (int)((N + T::BN - 1) / T::BN);
     const int tiles = p.tiles_m * p.tiles_n, parts = (T::BM / S::BM) * (T::BN / S::BN);
     p.whole = tiles / 256 * 256;
-    hipLaunchKernelGGL((gemm_i8_tail_kernel<S, decltype(o_tag)::value>), dim3((unsigned)(p.whole + (tiles - p.whole) * parts)),
-                       dim3(64 * T::WAVES), 0, stream, p);
+    auto go = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)(p.whole + (tiles - p.whole) * parts)), dim3(64 * T::WAVES), 0, stream, p);
+    };
+    if (shift)
+      go(gemm_i8_tail_kernel<Shifted<S>, decltype(o_tag)::value>);
+    else
+      go(gemm_i8_tail_kernel<S, decltype(o_tag)::value>);
   };
   auto pick = [&](auto o_tag) {
     if constexpr (decltype(o_tag)::value != OUT_PART) {

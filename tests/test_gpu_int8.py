@@ -210,6 +210,30 @@ def test_product_strided_and_padded(gpu, M, N, K, pa, pw, po):
         _check(one, v1, False)
 
 
+@pytest.mark.parametrize("at_a,pad_a,at_w,pad_w", [(0, 0, 0, 0), (16, 0, 112, 0), (0, -1, 48, 16), (96, 32, 0, -1), (80, -1, 64, -1)])
+@pytest.mark.parametrize("M,N,K", [(5, 100, 1168), (20, 300, 2064), (60, 515, 4112), (130, 700, 1296), (300, 2000, 1360), (700, 2000, 1552),
+                                   (1001, 2051, 1360), (1100, 4100, 2064), (4100, 4500, 1072), (2048, 5000, 1056)])
+def test_product_rows_off_the_cache_lines(gpu, M, N, K, at_a, pad_a, at_w, pad_w):
+    """Operands from byte at_* of a cache line, rows K + pad_* bytes apart (-1: to the next line); the
+    bytes around them are not zeros."""
+    announce(f"gemm_w8a8 {M}x{N}x{K} from {at_a} +{pad_a} and {at_w} +{pad_w}")
+    a, sa, w, sw, b = _operands(M, N, K, M + 2 * N + K)
+
+    def place(t, at, pad):
+        pitch = (K + 127) // 128 * 128 if pad < 0 else K + pad
+        buf = torch.full((256 + t.shape[0] * pitch,), 85, dtype=torch.int8, device="cuda")
+        start = -buf.data_ptr() % 128 + at
+        v = buf.as_strided(t.shape, (pitch, 1), start)
+        v.copy_(t)
+        assert v.data_ptr() % 128 == at
+        return v
+
+    av, wv = place(a, at_a, pad_a), place(w, at_w, pad_w)
+    v, _ = oracle.gemm_w8a8(a.numpy(), sa.numpy(), w.numpy(), sw.numpy(), b.numpy())
+    for dt in (F32, BF16):
+        _check(gpu.gemm_w8a8(av, sa.cuda(), wv, sw.cuda(), bias=b.cuda(), out_dtype=dt), v, True)
+
+
 @pytest.mark.parametrize("M", [1, 20, 300])
 def test_product_largest_sums(gpu, M):
     """Every product at its largest: the sum reaches 2^31 - 2^18 and -(2^31 - ...)."""
