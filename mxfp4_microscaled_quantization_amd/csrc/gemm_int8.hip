@@ -49,6 +49,7 @@ struct I8Params {
   int splits, ld_part;
   int whole;               // gemm_i8_tail_kernel: tiles in whole rounds
   int vec;                 // rows of the output start on 16-byte boundaries
+  int past;                // rows are stored past the caches
   int vec_channels;        // channel scales and biases are contiguous and 16-byte aligned
 };
 
@@ -174,6 +175,14 @@ __device__ __forceinline__ void store_channels(const I8Params& p, int m, int n, 
       if (n + 3 < p.N) o[3] = (uint16_t)(hi >> 16);
     }
   }
+}
+
+template <bool PAST, class V>
+__device__ __forceinline__ void store16(V* at, V v) {
+  if constexpr (PAST)
+    __builtin_nontemporal_store(v, at);
+  else
+    *at = v;
 }
 
 // What a workgroup leaves: finished bf16 or binary32 outputs, or the int32 sums of its part
@@ -375,6 +384,13 @@ __device__ __forceinline__ void i8_tile(Tile<MI, MJ, WM, WN, NA, NW, SHIFT>, con
     }
     return;
   }
+  // one branch around all the stores, so that the reads before them go out together
+  auto store_rows = [&](auto&& rows) {
+    if (p.past)
+      rows(std::true_type{});
+    else
+      rows(std::false_type{});
+  };
   const bool has_bias = p.bias != nullptr;
   float sw[MI][4], bs[MI][4];
 #pragma unroll
@@ -384,8 +400,7 @@ __device__ __forceinline__ void i8_tile(Tile<MI, MJ, WM, WN, NA, NW, SHIFT>, con
   if constexpr (OUT == OUT_BF16 && 16 * MJ >= RPI) {
     if (p.vec && n0 + BN <= p.N) {
       // park the wave's sub-tile in LDS (chunk c of row r at c ^ (r & (CPR - 1))) and store
-      // whole row segments, past the caches: the tile is not read again here, and the
-      // operands of the neighbouring tiles stay (about 1 %)
+      // whole row segments
       static_assert((CPR & (CPR - 1)) == 0 && CPR <= 64, "a power of two");
       static_assert(WAVES * 16 * MJ * RB <= LDS_BYTES, "staging fits the rings");
       __syncthreads();
@@ -405,13 +420,14 @@ __device__ __forceinline__ void i8_tile(Tile<MI, MJ, WM, WN, NA, NW, SHIFT>, con
         }
       }
       uint16_t* obase = static_cast<uint16_t*>(p.out) + (int64_t)mw * p.ld_out + nw;
+      store_rows([&](auto past) {
 #pragma unroll
-      for (uint32_t q = 0; q < 16 * MJ / RPI; ++q) {
-        const uint32_t row = RPI * q + lane / CPR, c = lane % CPR;
-        const v4i v = *reinterpret_cast<const v4i*>(sub + row * RB + ((c ^ (row & (CPR - 1))) << 4));
-        if (mw + (int)row < p.M)
-          __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(obase + (int64_t)row * p.ld_out + c * 8));
-      }
+        for (uint32_t q = 0; q < 16 * MJ / RPI; ++q) {
+          const uint32_t row = RPI * q + lane / CPR, c = lane % CPR;
+          const v4i v = *reinterpret_cast<const v4i*>(sub + row * RB + ((c ^ (row & (CPR - 1))) << 4));
+          if (mw + (int)row < p.M) store16<decltype(past)::value>(reinterpret_cast<v4i*>(obase + (int64_t)row * p.ld_out + c * 8), v);
+        }
+      });
       return;
     }
   }
@@ -442,13 +458,15 @@ __device__ __forceinline__ void i8_tile(Tile<MI, MJ, WM, WN, NA, NW, SHIFT>, con
     const int mb = mw + 16 * jb;
     if (whole) {
       constexpr int LPR = 4 * MI;                  // lanes per row, 4 columns each
+      store_rows([&](auto past) {
 #pragma unroll
-      for (int q = 0; q < 16 * CJ * LPR / 64; ++q) {
-        const int row = (int)(64 * q + lane) / LPR, col = (int)(64 * q + lane) % LPR * 4;
-        const v4f v = *reinterpret_cast<const v4f*>(sub + row * PITCH + col);
-        if (mb + row < p.M)
-          __builtin_nontemporal_store(v, reinterpret_cast<v4f*>(static_cast<float*>(p.out) + (int64_t)(mb + row) * p.ld_out + nw + col));
-      }
+        for (int q = 0; q < 16 * CJ * LPR / 64; ++q) {
+          const int row = (int)(64 * q + lane) / LPR, col = (int)(64 * q + lane) % LPR * 4;
+          const v4f v = *reinterpret_cast<const v4f*>(sub + row * PITCH + col);
+          if (mb + row < p.M)
+            store16<decltype(past)::value>(reinterpret_cast<v4f*>(static_cast<float*>(p.out) + (int64_t)(mb + row) * p.ld_out + nw + col), v);
+        }
+      });
     } else {
 #pragma unroll 4
       for (int q = 0; q < 16 * CJ * 16 * MI / 64; ++q) {
@@ -708,12 +726,17 @@ struct TileCost {
   int bm, bn;
   float fixed, per_window, again, off_lines;
 };
+// TILE_128x128_SHORT: rings of two windows, so that two workgroups fit a CU and one loads while the other
+// stores (13986 x 416 x 1664: 31 -> 24 us); with a longer K the deeper ring is faster (1024 x 4096 x 4096:
+// 31 us, 22.5).
+constexpr int kShortWindows = 4;
 constexpr float kLaunch = 3.0f, kDispatch = 1.07f;
-enum { TILE_256x256, TILE_128x256, TILE_128x128, TILE_64x128, TILE_128x64, TILE_64x64, TILE_64x32, TILE_32x64, TILE_32x32, TILES };
+enum { TILE_256x256, TILE_128x256, TILE_128x128, TILE_64x128, TILE_128x64, TILE_64x64, TILE_64x32, TILE_32x64, TILE_32x32, TILE_128x128_SHORT, TILES };
 constexpr TileCost kTileCost[TILES] = {
     {256, 256, 12.2f, 1.156f, 1.0f, 1.3f},  {128, 256, 11.7f, 0.728f, 1.0f, 1.25f}, {128, 128, 6.5f, 0.537f, 1.0f, 1.06f},
     {64, 128, 5.8f, 0.404f, 1.0f, 1.06f},   {128, 64, 5.8f, 0.404f, 1.0f, 1.06f},   {64, 64, 4.2f, 0.288f, 0.75f, 1.06f},
-    {64, 32, 4.0f, 0.222f, 0.75f, 1.06f},   {32, 64, 4.0f, 0.225f, 0.75f, 1.06f},   {32, 32, 3.2f, 0.162f, 0.75f, 1.06f}};
+    {64, 32, 4.0f, 0.222f, 0.75f, 1.06f},   {32, 64, 4.0f, 0.225f, 0.75f, 1.06f},   {32, 32, 3.2f, 0.162f, 0.75f, 1.06f},
+    {128, 128, 6.05f, 0.59f, 0.75f, 1.06f}};
 struct Plan {
   int tile, splits, tail;   // tail: the tile that the last round of 256 x 256 tiles is cut into, or -1
 };
@@ -735,6 +758,7 @@ Plan plan_w8a8(int64_t M, int64_t N, int64_t K, bool may_split) {
     const TileCost& c = kTileCost[t];
     const int64_t tiles = ((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
     if (t != TILE_256x256 && tiles > ((int64_t)1 << 22)) continue;   // threads of a launch stay below 2^32
+    if (t == TILE_128x128_SHORT && nwin > kShortWindows) continue;
     for (int s = 1; s <= (may_split ? 8 : 1); ++s) {
       if (s > 1 && (tiles * s > 256 || nwin < 8 * s)) break;
       const double further = (double)((tiles * s + 255) / 256 - 1);
@@ -783,6 +807,10 @@ I8Params i8_params(const int8_t* w, int64_t ld_w, const float* w_scales, int64_t
   p.nwin = (int)((K + kWin - 1) / kWin);
   auto aligned16 = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
   p.vec = (ld_out * (f32_out ? 4 : 2)) % 16 == 0 && aligned16(out);
+  // Rows of whole 64-byte pieces are stored past the caches: the output is not read again here, and
+  // the operands of the neighbouring tiles stay (75600 x 128 x 4000: 191 us, 215 through the caches);
+  // smaller pieces meet their other parts in the L2 (9000 x 512 x 9000: 107 us past the caches, 73).
+  p.past = (ld_out * (f32_out ? 4 : 2)) % 64 == 0 && reinterpret_cast<uintptr_t>(out) % 64 == 0;
   p.vec_channels = inc_ws == 1 && aligned16(w_scales) && aligned16(bias);
   p.splits = 1;
   return p;
@@ -872,7 +900,8 @@ hipError_t launch_gemm_w8a8(const int8_t* a, int64_t ld_a, const float* a_scales
       case TILE_64x64: return tile(Tile<2, 2, 2, 2, 4, 4>{}, o_tag);
       case TILE_64x32: return tile(Tile<1, 2, 2, 2, 6, 6>{}, o_tag);
       case TILE_32x64: return tile(Tile<2, 1, 2, 2, 6, 6>{}, o_tag);
-      default: return tile(Tile<1, 1, 2, 2, 8, 8>{}, o_tag);
+      case TILE_32x32: return tile(Tile<1, 1, 2, 2, 8, 8>{}, o_tag);
+      default: return tile(Tile<2, 4, 2, 4, 2, 2>{}, o_tag);
     }
   };
   if (p.splits > 1) {

@@ -172,7 +172,10 @@ SHAPES = [(1, 1, 16), (1, 5120, 1360), (2, 3, 131056), (1, 17, 4096), (3, 16, 64
           (256, 5120, 8192), (500, 5120, 400), (500, 770, 16000), (700, 13824, 144), (1300, 5120, 272), (2100, 5000, 160),
           (64, 256, 131056),
           # a last round of the largest tile cut into halves and quarters, ragged at both edges
-          (4100, 4500, 48), (3900, 4700, 1040), (4400, 5000, 400), (4099, 4501, 160)]
+          (4100, 4500, 48), (3900, 4700, 1040), (4400, 5000, 400), (4099, 4501, 160),
+          # a short K: the largest tile, and the one with two workgroups on a CU, with every output alignment
+          (3600, 3584, 128), (2100, 2048, 512), (2100, 2056, 400), (2100, 2052, 64), (2100, 2050, 272), (1500, 1504, 240), (1500, 1502, 240),
+          (3000, 3000, 208)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
