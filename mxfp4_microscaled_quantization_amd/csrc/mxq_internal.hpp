@@ -78,7 +78,7 @@ struct QkNormParams {
   const float *cos, *sin;
   const int64_t* positions;   // or null: token t has position t
   int head_dim, rot_dim, w_f32;
-  int runs_q;                 // blockIdx.y below it: queries
+  int runs_q;                 // workgroups (blockIdx.y, or .x for pairs) below it: queries
   float eps, inv_dim;
 };
 hipError_t launch_qk_norm_rope(const QkNormParams& p, bool f32, bool quant, bool halves, hipStream_t stream);

@@ -168,6 +168,43 @@ def test_results_do_not_depend_on_the_batch(gpu):
                 assert all(torch.equal(a, b[lo:hi]) for a, b in zip(part8, full8))
 
 
+@pytest.mark.parametrize("Hq,Hk,D,R", [(1, 1, 128, 128), (2, 1, 80, 40), (4, 4, 128, 64), (7, 1, 104, 104), (8, 8, 64, 64), (3, 0, 32, 32),
+                                       (0, 2, 256, 256), (3, 1, 256, 128), (1, 1, 512, 512), (1, 1, 8, 8), (16, 0, 48, 0)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_few_heads_of_many_tokens(gpu, Hq, Hk, D, R, dtype):
+    """Waves that take pairs of tokens and heads against the oracle, and against parts of the batch
+    that are too small for them; positions outside the table; in place."""
+    announce(f"qk_norm_rope {Hq}+{Hk} heads x {D}, rotated {R}, {dtype}")
+    T = 1501
+    for style in ("interleaved", "halves"):
+        qkv, q, k, wq, wk, cos, sin, pos = _inputs(T, Hq, Hk, D, R, 100, dtype, dtype, D + Hq)
+        if R:
+            pos[5], pos[700], pos[T - 1] = -1, 100, 2 ** 40
+        kw = dict(eps=1e-6, style=style)
+        full = gpu.qk_norm_rope(q, k, wq, wk, cos, sin, positions=pos, **kw)
+        full8 = gpu.quantize_qk_norm_rope(q, k, wq, wk, cos, sin, positions=pos, **kw)
+        good = torch.ones(T, dtype=torch.bool)
+        if R:
+            good[[5, 700, T - 1]] = False
+        safe = pos.cpu().masked_fill(~good, 0) if R else None
+        cut = lambda lo: pos[lo:lo + 400] if R else None
+        for o, x, w in ((full[0], q, wq), (full[1], k, wk)):
+            if x.shape[1]:
+                ref, size = _oracle(x, w, cos, sin, safe, 1e-6, style)
+                _check(o.cpu()[good], ref[good.numpy()], size[good.numpy()])
+                assert bool(o[~good][..., :R].isnan().all())
+        bits = lambda t: t.view({1: torch.int8, 2: torch.int16, 4: torch.int32}[t.element_size()])
+        for lo in range(0, T, 400):
+            part = gpu.qk_norm_rope(q[lo:lo + 400], k[lo:lo + 400], wq, wk, cos, sin, positions=cut(lo), **kw)
+            part8 = gpu.quantize_qk_norm_rope(q[lo:lo + 400], k[lo:lo + 400], wq, wk, cos, sin, positions=cut(lo), **kw)
+            for a, b in zip((*part, *part8), (*full, *full8)):
+                assert torch.equal(bits(a), bits(b[lo:lo + 400]))
+        before = qkv.clone()
+        gpu.qk_norm_rope(q, k, wq, wk, cos, sin, positions=pos, out_q=q, out_k=k, **kw)
+        assert torch.equal(bits(q), bits(full[0])) and torch.equal(bits(k), bits(full[1]))
+        assert torch.equal(qkv[:, (Hq + Hk) * D:], before[:, (Hq + Hk) * D:])
+
+
 def test_one_head_with_any_head_pitch(gpu):
     """A single head has no head pitch: a huge one through the C ABI changes nothing and
     writes nothing else."""
