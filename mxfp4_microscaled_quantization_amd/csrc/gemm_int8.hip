@@ -250,13 +250,17 @@ __device__ __forceinline__ void i8_tile(Tile<MI, MJ, WM, WN, NA, NW, SHIFT>, con
   // SHIFT: block w of a row is its cache line w, which starts `ph` bytes before window w; ph is
   // the same every 8 rows, since pitches are multiples of 16
   const uint32_t ph_a = (off_a + (SHIFT ? drow * p.ld_a : 0u)) & 127u, ph_w = (off_w + (SHIFT ? drow * p.ld_w : 0u)) & 127u;
-  const uint32_t row_a = drow * p.ld_a + off_a - ph_a, row_w = drow * p.ld_w + off_w - ph_w;
-  const uint32_t va0 = row_a + chunk0, va1 = row_a + chunk1, vw0 = row_w + chunk0, vw1 = row_w + chunk1;
+  // its chunks lie as those of window w would, so that the fragment reads stay free of conflicts:
+  // ka, kw: the K (from that of the block's window) that a lane fetches, negative before the window
+  auto in_line = [](uint32_t chunk, uint32_t ph) { return SHIFT ? ((chunk + ph) & 127u) - ph : chunk; };
+  const uint32_t ka0 = in_line(chunk0, ph_a), ka1 = in_line(chunk1, ph_a), kw0 = in_line(chunk0, ph_w), kw1 = in_line(chunk1, ph_w);
+  const uint32_t row_a = drow * p.ld_a + off_a, row_w = drow * p.ld_w + off_w;
+  const uint32_t va0 = row_a + ka0, va1 = row_a + ka1, vw0 = row_w + kw0, vw1 = row_w + kw1;
   const bool in0 = chunk0 < last_bytes, in1 = chunk1 < last_bytes;   // of the last window
   auto issue_a = [&](int w, uint32_t slot, int j) {
     const uint32_t line = wave * LA + j;
     const bool odd = LA % 2 == 0 ? j & 1 : line & 1;
-    const bool in = SHIFT ? (uint32_t)w * kWin + (odd ? chunk1 : chunk0) - ph_a < (uint32_t)K
+    const bool in = SHIFT ? (uint32_t)w * kWin + (odd ? ka1 : ka0) < (uint32_t)K
                           : w + 1 < nwin || (odd ? in1 : in0);
     line_to_lds(make_rsrc(base_a, SHIFT || w < nwin ? bytes_a : 0u), lds + slot * A_TILE + line * 1024,
                 in ? (odd ? va1 : va0) : kOutside, (uint32_t)w * kWin + line * 8 * p.ld_a);
@@ -264,7 +268,7 @@ __device__ __forceinline__ void i8_tile(Tile<MI, MJ, WM, WN, NA, NW, SHIFT>, con
   auto issue_w = [&](int w, uint32_t slot, int j) {
     const uint32_t line = wave * LW + j;
     const bool odd = LW % 2 == 0 ? j & 1 : line & 1;
-    const bool in = !SHIFT || (uint32_t)w * kWin + (odd ? chunk1 : chunk0) - ph_w < (uint32_t)K;
+    const bool in = !SHIFT || (uint32_t)w * kWin + (odd ? kw1 : kw0) < (uint32_t)K;
     line_to_lds(make_rsrc(base_w, SHIFT || w < nwin ? bytes_w : 0u), lds + W_BASE + slot * W_TILE + line * 1024,
                 in ? (odd ? vw1 : vw0) : kOutside, (uint32_t)w * kWin + line * 8 * p.ld_w);
   };
@@ -279,14 +283,14 @@ __device__ __forceinline__ void i8_tile(Tile<MI, MJ, WM, WN, NA, NW, SHIFT>, con
   // step-t fragments of the window in ring slots u mod NA, u mod NW: weight rows, then
   // activation rows; after(k) follows read k.  A lane reads chunk g + 4t of rows r16 + 16 i,
   // whose swizzle is that of r16: one offset for t = 0, and the same with bit 6 turned for t = 1
+  const uint32_t frag = lds_slot(r16, g);
   // SHIFT: the chunks of a row are counted from its block, and those past 7 are in the next
   const uint32_t ca = g + (((off_a + r16 * p.ld_a) & 127u) >> 4), cw = g + (((off_w + r16 * p.ld_w) & 127u) >> 4);
-  const uint32_t frag_a = lds_slot(r16, SHIFT ? ca & 7u : g) + wm * (16 * MJ * 128);
-  const uint32_t frag_w = lds_slot(r16, SHIFT ? cw & 7u : g) + wn * (16 * MI * 128) + W_BASE;
   auto read = [&](v4i(&f)[RD], uint32_t u, int t, auto&& after) {
-    const bool over_a = SHIFT && ca + 4 * t > 7, over_w = SHIFT && cw + 4 * t > 7;
-    const uint8_t* la = lds + ((frag_a ^ (64u * t)) + (over_a ? (u + 1) % NA : u % NA) * A_TILE);
-    const uint8_t* lw = lds + ((frag_w ^ (64u * t)) + (over_w ? (u + 1) % NW : u % NW) * W_TILE);
+    const uint32_t at = frag ^ (64u * t);
+    const uint32_t ua = SHIFT && ca + 4 * t > 7 ? (u + 1) % NA : u % NA, uw = SHIFT && cw + 4 * t > 7 ? (u + 1) % NW : u % NW;
+    const uint8_t* la = lds + (at + wm * (16 * MJ * 128) + ua * A_TILE);
+    const uint8_t* lw = lds + (at + wn * (16 * MI * 128) + W_BASE + uw * W_TILE);
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       f[i] = *reinterpret_cast<const v4i*>(lw + 2048 * i);
