@@ -339,7 +339,8 @@ mxq_status mxq_dequantize_int8(const int8_t* codes, int64_t ld_codes, const floa
  *   v = fl32( t * w_scales[n] ), or with a bias the fused multiply-add t * w_scales[n] + bias[n]
  *   rounded once;  out = v as binary32 (MXQ_F32) or bf16_RNE(v) (MXQ_BF16).
  * a : M x K int8, pitch ld_a bytes; w : N x K int8, pitch ld_w bytes.  Bases and pitches
- *     multiples of 16, pitches below 2^23.  Any int8 codes, -128 included.
+ *     multiples of 16, pitches below 2^23 (fastest where both are multiples of 128).  Any int8
+ *     codes, -128 included.
  * a_scales, w_scales : float, element m (n) at m * inc_as (n * inc_ws), increments >= 0 (0:
  *     one scale for all).  bias : float[N] or NULL.
  * out : M x N of out_dt, pitch ld_out elements (>= N), naturally aligned.
