@@ -455,12 +455,22 @@ def dequantize_fp8(q, a_scale: float, out=None) -> torch.Tensor:
 
 # the raw stream handle without building a Stream object (2 us of the 10 us of a small call); None without a GPU build
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# torch.cuda.current_device without its check that CUDA is initialized: the tensors are there
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+# allocations by explicit strides take 1.3 us, by shape alone 1.7
+_empty = torch.empty_strided
+
+
+def _there(t, name, device):
+    """_dev, in fewer steps for a plain tensor on the device of one that _dev has seen."""
+    if device is None or type(t) is not torch.Tensor or t.device != device:
+        _dev(t, name, device)
 
 
 def _call(fn, device, *args):
     """``fn(*args, stream)`` with torch's current stream of ``device``, checked."""
     index = device.index
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
@@ -471,7 +481,7 @@ def _call(fn, device, *args):
 
 def _matrix(t, name, dtype, device=None, shape=None):
     """A 2-D GPU tensor of ``dtype`` (or one of several) with contiguous rows: its row pitch."""
-    _dev(t, name, device)
+    _there(t, name, device)
     if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
         raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
     if t.dim() != 2:
@@ -487,7 +497,7 @@ def _matrix(t, name, dtype, device=None, shape=None):
 
 def _vector(t, name, n, device, dtype=torch.float32):
     """A 1-D GPU tensor of ``n`` elements: the distance between them (0 for an expanded one)."""
-    _dev(t, name, device)
+    _there(t, name, device)
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
     if t.shape != (n,):
@@ -515,11 +525,11 @@ def quantize_int8(x, codes=None, scales=None):
     ld = _matrix(x, "x", _FLOATS)
     R, K = x.shape
     if codes is None:
-        codes, ldc = torch.empty((R, K), dtype=torch.int8, device=x.device), K
+        codes, ldc = _empty((R, K), (K, 1), dtype=torch.int8, device=x.device), K
     else:
         ldc = _matrix(codes, "codes", torch.int8, x.device, (R, K))
     if scales is None:
-        scales = torch.empty(R, dtype=torch.float32, device=x.device)
+        scales = _empty((R,), (1,), dtype=torch.float32, device=x.device)
     else:
         _flat(scales, "scales", R, x.device)
     _call(lib.mxq_quantize_int8, x.device, x.data_ptr(), _dtype_code(x), R, K, ld, codes.data_ptr(), ldc,
@@ -533,7 +543,7 @@ def dequantize_int8(codes, scales, out=None):
     R, K = codes.shape
     _flat(scales, "scales", R, codes.device)
     if out is None:
-        out, ld = torch.empty((R, K), dtype=torch.bfloat16, device=codes.device), K
+        out, ld = _empty((R, K), (K, 1), dtype=torch.bfloat16, device=codes.device), K
     else:
         ld = _matrix(out, "out", torch.bfloat16, codes.device, (R, K))
     _call(lib.mxq_dequantize_int8, codes.device, codes.data_ptr(), ldc, scales.data_ptr(), R, K, out.data_ptr(), ld)
@@ -544,7 +554,7 @@ def _w8_out(M, N, device, out, out_dtype):
     if out is None:
         if out_dtype not in _FLOATS:
             raise ValueError("out_dtype must be bfloat16 or float32")
-        return torch.empty((M, N), dtype=out_dtype, device=device), N
+        return _empty((M, N), (N, 1), dtype=out_dtype, device=device), N
     return out, _matrix(out, "out", _FLOATS, device, (M, N))
 
 
@@ -608,7 +618,7 @@ ROPE_STYLES = {"interleaved": 0, "halves": 1}
 
 def _heads(t, name, dtype=None, device=None, shape=None):
     """A 3-D GPU tensor [tokens, heads, head_dim] with contiguous heads: (token pitch, head pitch)."""
-    _dev(t, name, device)
+    _there(t, name, device)
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
     if t.dim() != 3:
@@ -636,7 +646,7 @@ def _qk_inputs(q, k, q_weight, k_weight, cos, sin, positions, eps, style):
     w_dt = None
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
-            _dev(w, name, dev)
+            _there(w, name, dev)
             dtype = w.dtype
             if dtype not in _FLOATS:
                 raise ValueError(f"{name} must be bfloat16 or float32")
@@ -665,7 +675,7 @@ def _qk_inputs(q, k, q_weight, k_weight, cos, sin, positions, eps, style):
 def _head_out(x, out, name):
     if out is None:
         T, H, D = x.shape
-        return torch.empty((T, H, D), dtype=x.dtype, device=x.device), (H * D, D)
+        return _empty((T, H, D), (H * D, D, 1), dtype=x.dtype, device=x.device), (H * D, D)
     return out, _heads(out, name, x.dtype, x.device, x.shape)
 
 
@@ -694,8 +704,8 @@ def quantize_qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions=None, ep
     outs = []
     for x in (q, k):
         T, H, D = x.shape
-        outs += [torch.empty((T, H, D), dtype=torch.int8, device=x.device),
-                 torch.empty((T, H), dtype=torch.float32, device=x.device)]
+        outs += [_empty((T, H, D), (H * D, D, 1), dtype=torch.int8, device=x.device),
+                 _empty((T, H), (H, 1), dtype=torch.float32, device=x.device)]
     qc, qs, kc, ks = outs
     D, Hq, Hk = q.shape[2], q.shape[1], k.shape[1]
     _call(lib.mxq_quantize_qk_norm_rope, q.device, *args, qc.data_ptr(), Hq * D, D, qs.data_ptr(), Hq,
