@@ -442,9 +442,8 @@ __device__ __forceinline__ void i8_tile(Tile<MI, MJ, WM, WN, NA, NW, SHIFT>, con
     }
   }
   // binary32 outputs, and rows that are not 16-byte aligned or end inside the tile: the same
-  // through a binary32 image of CJ blocks of rows, stored in the order of the rows (single
-  // elements where a row has no alignment: 1001 x 1360 x 2051 to binary32 took 17.2 us with
-  // each lane storing its own columns, 14.8 here)
+  // through a binary32 image of CJ blocks of rows, stored in the order of the rows
+  // (1001 x 1360 x 2051 to binary32 took 2.4 us longer with each lane storing its own columns)
   constexpr int PITCH = 16 * MI + 4;               // floats per row in LDS
   constexpr int FIT = (int)(LDS_BYTES / (WAVES * 16 * PITCH * 4));
   constexpr int CJ = FIT >= MJ ? MJ : FIT >= 4 ? 4 : FIT >= 2 ? 2 : 1;
@@ -477,6 +476,40 @@ __device__ __forceinline__ void i8_tile(Tile<MI, MJ, WM, WN, NA, NW, SHIFT>, con
             store16<decltype(past)::value>(reinterpret_cast<v4f*>(static_cast<float*>(p.out) + (int64_t)(mb + row) * p.ld_out + nw + col), v);
         }
       });
+    } else if (n0 + BN <= p.N) {
+      // 16 bytes from the first 16-byte boundary of each row on, then the E elements that are left
+      // over at its two ends (9000 x 512 x 9001: 86 us; with single elements 103, with pairs 120)
+      using Elem = std::conditional_t<OUT == OUT_F32, float, uint16_t>;
+      constexpr int W = 16 * MI, E = 16 / (int)sizeof(Elem), GROUPS = 16 * CJ * W / E, REST = 16 * CJ * E;
+      auto row_at = [&](int row) { return static_cast<Elem*>(p.out) + (int64_t)(mb + row) * p.ld_out + nw; };
+      auto to_boundary = [&](const Elem* o) { return (int)(-(reinterpret_cast<uintptr_t>(o) / sizeof(Elem)) & (E - 1)); };
+#pragma unroll 4
+      for (int q = 0; q < (GROUPS + 63) / 64; ++q) {
+        const int at = 64 * q + (int)lane, row = at / (W / E);
+        Elem* o = row_at(row);
+        const int col = at % (W / E) * E + to_boundary(o);
+        if (at < GROUPS && mb + row < p.M && col + E <= W) {
+          const float* v = sub + row * PITCH + col;
+          if constexpr (OUT == OUT_F32)
+            *reinterpret_cast<v4f*>(o + col) = v4f{v[0], v[1], v[2], v[3]};
+          else
+            *reinterpret_cast<v4u*>(o + col) =
+                v4u{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+        }
+      }
+#pragma unroll 4
+      for (int q = 0; q < (REST + 63) / 64; ++q) {
+        const int at = 64 * q + (int)lane, row = at / E, e = at % E;
+        Elem* o = row_at(row);
+        const int head = to_boundary(o), col = e < head ? e : W - E + e;
+        if (at < REST && mb + row < p.M && head > 0) {
+          const float v = sub[row * PITCH + col];
+          if constexpr (OUT == OUT_F32)
+            o[col] = v;
+          else
+            o[col] = (uint16_t)pack_bf16x2(v, 0.0f);
+        }
+      }
     } else {
 #pragma unroll 4
       for (int q = 0; q < 16 * CJ * 16 * MI / 64; ++q) {
