@@ -24,8 +24,8 @@
 //    fragment read takes its chunk from block w or w + 1, which the ring holds both (pitches
 //    are multiples of 16, so that a row's offset in its line is the same every 8 rows).
 //
-// What bounds it: power on large shapes.  75600 x 5120 x 13824 takes 3.81 to 4.09 ms on different
-// GPUs, 2.61 to 2.81 POP/s, with the matrix cores 75 % busy; the same MFMAs from registers
+// What bounds it: power on large shapes.  75600 x 5120 x 13824 takes 3.75 to 4.09 ms on different
+// GPUs, 2.61 to 2.86 POP/s, with the matrix cores 75 % busy; the same MFMAs from registers
 // alone run at 3.87 POP/s on such codes.  Where each CU has a tile or two, the latencies at a tile's
 // ends and the 64 bytes a clock that a CU's loads into LDS take (512 x 5120 x 5120: 28 us, 0.97
 // POP/s); with few rows the weights' bytes (48 x 13824 x 5120, K in 6 parts: 18.7 us, 3.8 TB/s).
