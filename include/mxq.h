@@ -406,8 +406,9 @@ typedef enum {
  *           Either may have 0 heads (its other arguments are then ignored).
  * w_q, w_k: head_dim weights of w_dt each, or NULL for 1.
  * cos, sin: table_rows x rot_dim / 2 float, pitch ld_table; unused when rot_dim == 0.
- * out_q, out_k : like q and k, of `dt`.  An output may be its input with the same pitches;
- *           no other overlap.
+ * out_q, out_k : like q and k, of `dt`, no two heads of an output on the same memory
+ *           (MXQ_ERR_INVALID_ARG).  An output may be its input with the same pitches; no other
+ *           overlap.
  * head_dim: a multiple of 8 up to 512; rot_dim: a multiple of 8 up to head_dim; heads up
  *           to 65536 each.  Bases 16-byte aligned; all pitches of q, k, out_q, out_k
  *           multiples of 16 bytes and not negative; ld_table % 4 == 0.  The heads of one

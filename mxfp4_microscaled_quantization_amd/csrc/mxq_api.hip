@@ -158,6 +158,24 @@ struct HeadArgs {
   int64_t ld_s;
 };
 
+// Whether every (token, head) has `width` elements of its own at token * ld + head * hs, both
+// pitches >= width.  The usual layouts hold all heads of a token between two tokens, or all tokens
+// of a head between two heads.  In any other, places meet where some difference of a positive
+// number of heads and of tokens comes closer than `width`: for each number on the axis with fewer,
+// only the two multiples of the other pitch around it can (at most 65535 of them).
+bool heads_apart(int64_t tokens, int64_t heads, int64_t ld, int64_t hs, int64_t width) {
+  if (tokens <= 1 || heads <= 1 || ld >= (heads - 1) * hs + width || hs >= (tokens - 1) * ld + width) return true;
+  const bool by_head = heads <= tokens;
+  const int64_t few = by_head ? heads : tokens, many = by_head ? tokens : heads;
+  const int64_t step = by_head ? hs : ld, other = by_head ? ld : hs;
+  for (int64_t i = 1; i < few; ++i)
+    for (int64_t j = i * step / other, end = j + 2; j < end; ++j) {
+      const int64_t off = i * step - j * other;
+      if (j >= 1 && j < many && off < width && -off < width) return false;
+    }
+  return true;
+}
+
 mxq_status check_heads(const char* fn, const HeadArgs& h, int bytes, int out_bytes, int out_align, int w_bytes,
                        int64_t tokens, int64_t head_dim, bool quant) {
   if (h.heads < 0 || h.heads > 65536)
@@ -175,9 +193,10 @@ mxq_status check_heads(const char* fn, const HeadArgs& h, int bytes, int out_byt
     return fail(MXQ_ERR_INVALID_ARG, "%s: %s base and pitches must be 16-byte aligned", fn, h.name);
   if (!aligned(h.out, (uintptr_t)out_align) || h.ld_o * out_bytes % out_align != 0 || h.hs_o * out_bytes % out_align != 0)
     return fail(MXQ_ERR_INVALID_ARG, "%s: output base and pitches of %s must be %d-byte aligned", fn, h.name, out_align);
-  // every (token, head) has a place of its own in the output
   if ((h.heads > 1 && h.hs_o < head_dim) || (tokens > 1 && h.ld_o < head_dim))
     return fail(MXQ_ERR_INVALID_ARG, "%s: output pitches of %s below head_dim", fn, h.name);
+  if (!heads_apart(tokens, h.heads, h.ld_o, h.hs_o, head_dim))
+    return fail(MXQ_ERR_INVALID_ARG, "%s: output heads of %s overlap", fn, h.name);
   if (h.w && !aligned(h.w, (uintptr_t)(4 * w_bytes)))
     return fail(MXQ_ERR_INVALID_ARG, "%s: w_%s must be %d-byte aligned", fn, h.name, 4 * w_bytes);
   if (quant) {
