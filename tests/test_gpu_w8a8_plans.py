@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from helpers import announce
-from w8a8_shapes import PLANS
+from w8a8_shapes import AT_LARGEST_PITCH, LARGEST_PITCH, PLANS
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
@@ -41,3 +41,17 @@ def _check(gpu, a, sa, w, sw, b):
 def test_every_kernel(gpu, M, N, K, tile, parts, tail, off):
     announce(f"gemm_w8a8 {M}x{N}x{K}: {tile} in {parts} parts, last round {tail}, off the lines {off}")
     _check(gpu, *_operands(M, N, K))
+
+
+@pytest.mark.parametrize("M,N,K,tile,parts,tail,off", AT_LARGEST_PITCH)
+def test_largest_tiles_with_the_largest_row_pitch(gpu, M, N, K, tile, parts, tail, off):
+    """Both operands as rows 8 MB apart of one buffer of 30 GB."""
+    announce(f"gemm_w8a8 {M}x{N}x{K}: {tile}, rows {LARGEST_PITCH} bytes apart")
+    a, sa, w, sw, b = _operands(M, N, K)
+    buf = torch.empty(max(M, N) * LARGEST_PITCH, dtype=torch.int8, device="cuda")
+    av, wv = buf.as_strided((M, K), (LARGEST_PITCH, 1), 0), buf.as_strided((N, K), (LARGEST_PITCH, 1), 4096)
+    av.copy_(a)
+    wv.copy_(w)
+    for dtype in (F32, BF16):
+        assert torch.equal(gpu.gemm_w8a8(av, sa, wv, sw, bias=b, out_dtype=dtype), gpu.gemm_w8a8(a, sa, w, sw, bias=b, out_dtype=dtype))
+    _check(gpu, av, sa, wv, sw, b)

@@ -10,7 +10,7 @@ import subprocess
 
 import pytest
 
-from w8a8_shapes import PLANS
+from w8a8_shapes import AT_LARGEST_PITCH, LARGEST_PITCH, PLANS
 
 SRC = os.path.join(os.path.dirname(os.path.abspath(__file__)), "native", "w8a8_plans.cpp")
 
@@ -36,6 +36,8 @@ def test_listed_shapes_take_the_kernels_they_name(plans):
     got = plans([(M, N, K, 1, 0, K) for M, N, K, *_ in PLANS])
     wrong = [(p, g) for p, g in zip(PLANS, got) if tuple(p[3:]) != g]
     assert not wrong
+    got = plans([(M, N, K, 1, 0, LARGEST_PITCH) for M, N, K, *_ in AT_LARGEST_PITCH])
+    assert got == [tuple(p[3:]) for p in AT_LARGEST_PITCH]
 
 
 def _kind(plan):
