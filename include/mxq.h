@@ -394,8 +394,10 @@ typedef enum {
 
 /*
  * mxq_qk_norm_rope -- root-mean-square norm of every query and key head with the position
- * rotation in the same pass (the step between the QKV projection and attention in FLUX- and
- * Wan-like blocks).  For each token and head x of head_dim elements, in binary32:
+ * rotation in the same pass (the step between the QKV projection and attention in blocks that
+ * norm each head, as FLUX does; Wan norms the whole query and the whole key of a token before
+ * the split into heads, with a weight of that width: another operator, which this is not).
+ * For each token and head x of head_dim elements, in binary32:
  *   r = 1 / sqrt( sum x^2 / head_dim + eps );  y = (x * r) * w;
  *   pairs (a, b) of the first rot_dim elements -> (a c - b s, b c + a s), c and s from row
  *   p of cos and sin, column i (mxq_rope_style), p = positions[token] (token if NULL);

@@ -681,7 +681,8 @@ def _head_out(x, out, name):
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions=None, eps=1e-6, style="interleaved", out_q=None,
                  out_k=None):
-    """Root-mean-square norm of every query and key head, with the position rotation in the same pass.
+    """Root-mean-square norm of every query and key head by itself (not of a token's whole query or key), with the
+    position rotation in the same pass.
 
     ``q`` [T, Hq, D] and ``k`` [T, Hk, D], bf16 or fp32, views of a QKV projection's output as they are (heads
     contiguous, D a multiple of 8 up to 512).  ``q_weight``, ``k_weight``: [D] or None.  ``cos``, ``sin``: float32
