@@ -402,8 +402,10 @@ typedef enum {
  *   pairs (a, b) of the first rot_dim elements -> (a c - b s, b c + a s), c and s from row
  *   p of cos and sin, column i (mxq_rope_style), p = positions[token] (token if NULL);
  * rounded to `dt` once.  The sum of squares is formed in binary32: a head where it
- * overflows comes out as zeros.  The rotated elements of a token whose position is outside
- * [0, table_rows) come out as NaN, and no memory outside the table is read for it.
+ * overflows comes out as zeros; with eps == 0 one whose mean of squares is 0 there (all
+ * zeros, or elements of about 2^-75 and less) as NaN or infinities.  Other heads are
+ * unaffected.  The rotated elements of a token whose position is outside [0, table_rows)
+ * come out as NaN, and no memory outside the table is read for it.
  * q, k    : tokens x heads x head_dim of `dt`; element (t, h, d) at t * ld + h * hs + d.
  *           Either may have 0 heads (its other arguments are then ignored).
  * w_q, w_k: head_dim weights of w_dt each, or NULL for 1.
