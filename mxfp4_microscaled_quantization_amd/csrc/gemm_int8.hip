@@ -24,11 +24,13 @@
 //    fragment read takes its chunk from block w or w + 1, which the ring holds both (pitches
 //    are multiples of 16, so that a row's offset in its line is the same every 8 rows).
 //
-// What bounds it: power on large shapes.  75600 x 5120 x 13824 takes 3.75 to 4.09 ms on different
-// GPUs, 2.61 to 2.86 POP/s, with the matrix cores 75 % busy; the same MFMAs from registers
-// alone run at 3.87 POP/s on such codes.  Where each CU has a tile or two, the latencies at a tile's
-// ends and the 64 bytes a clock that a CU's loads into LDS take (512 x 5120 x 5120: 28 us, 0.97
-// POP/s); with few rows the weights' bytes (48 x 13824 x 5120, K in 6 parts: 18.0 us, 4.0 TB/s).
+// What bounds it: power on large shapes.  75600 x 5120 x 13824 takes 3.93 to 3.95 ms on codes of
+// normal values, 4.05 ms on uniform ones, and 3.75 to 4.18 ms over all GPUs and profiled runs (2.56 to
+// 2.86 POP/s), with the matrix cores 75 % busy; the same MFMAs from registers alone run at 3.87
+// POP/s on such codes.  Where each CU has a tile or two, the latencies at a tile's ends and the 64
+// bytes a clock that a CU's loads into LDS take (512 x 5120 x 5120: 28 us, 0.96 POP/s); with few
+// rows the weights' bytes (48 x 13824 x 5120, K in 6 parts: 20.5 us, 3.5 TB/s; 18.0 us where the
+// memory-side cache holds the weights).
 #include <type_traits>
 #include <utility>
 
@@ -595,9 +597,11 @@ __global__ __launch_bounds__(256) void i8_reduce_kernel(I8Params p) {
 // sums meet (integers: the order changes nothing).  The workgroups start at windows spread
 // over K: started together, they would read the same columns of all rows at once, which a
 // row pitch of a power of two maps to a few memory channels (1 x 8192 x 4096: 12.0 -> 9.0 us).
-// Bound by the weights' bytes: 1 x 5120 x 13824 12.1 us with the next call's launch behind it, 5.8 TB/s
-// (12.7 us by itself); with the activations made here 1 x 13824 x 5120 13.5 us (two launches 15.7).  For 9 to 64 tokens such a kernel with 2 to 8 lines of
-// activations is no faster than the tiles (16 x 5120 x 5120: 8.9 and 9.0 us; 48 x 13824 x 5120: 24 and 21).
+// Bound by the weights' bytes: 1 x 5120 x 13824 takes 15.0 us, 4.7 TB/s, with the next call's launch behind
+// it (12.1 us where the memory-side cache holds the weights); with the activations made here 1 x 13824 x 5120
+// takes 16.6 us, two launches 18.5 (13.5 and 15.7).  For 9 to 64 tokens such a kernel with 2 to 8 lines of
+// activations is no faster than the tiles (weights not in a cache, side by side: 16 x 5120 x 5120 8.9 and 9.0
+// us, 48 x 13824 x 5120 24 and 21).
 //
 // A_BF16, A_F32: the activations come unquantized, and every workgroup makes the codes of
 // all tokens itself, into LDS, while its first weight windows are on their way: at a few KB

@@ -6,9 +6,11 @@
 // one row, C units of 8 elements each, all loads first, one reduction (DPP inside a wave,
 // LDS across the W waves), then the codes.  Rows past T * 8 * C elements of the largest
 // variant are read twice; rows of up to 32 units (heads) share a wave.
-// Measured: 75600 x 13824 bf16 0.51 ms (6.1 TB/s; a row over 4 waves x 8 units 0.52, over
-// 16 x 2 0.57), 75600 x 5120 0.18 ms (6.4 TB/s), 300000 x 128 0.0185 ms (6.2 TB/s; a
-// wave for each row 0.058); dequantization of 300000 x 128 0.018 ms (6.4 TB/s).
+// Measured: 75600 x 13824 bf16 0.516 ms (6.1 TB/s; a row over 4 waves x 8 units 0.52, over
+// 16 x 2 0.57) and binary32 0.888 ms (5.9 TB/s), 75600 x 5120 bf16 0.184 ms (6.3 TB/s) and
+// binary32 0.326 ms (5.9 TB/s), 300000 x 128 bf16 0.022 ms (5.2 TB/s; 0.0185 from the memory-side
+// cache, a wave for each row 0.058); dequantization of 75600 x 13824 0.567 ms (5.5 TB/s), of
+// 300000 x 128 0.0228 ms (5.1 TB/s; 0.018 from the memory-side cache).
 #include <type_traits>
 
 #include "mxq_int8.hpp"

@@ -15,9 +15,13 @@
 // lane swaps inside the G lanes.  A lane's 8 elements are 4 whole pairs: consecutive ones
 // when interleaved, 4 from each half otherwise, so no partner comes from another lane.  Tokens of
 // few heads would leave most of such a wave empty: there a wave takes pairs (token, head).
-// Measured, 75600 tokens x (40 + 40) heads x 128 in bf16: 0.55 ms, 5.6 TB/s (0.61 ms with
-// 64-bit addresses for each lane and queries and keys in one loop); 57344 x (24 + 24) x 128
-// to 8-bit codes: 0.185 ms, 5.7 TB/s.
+// Measured, 75600 tokens x (40 + 40) heads x 128 in bf16: 0.555 ms in either style, 5.6 TB/s (0.61 ms
+// with 64-bit addresses for each lane and queries and keys in one loop), to 8-bit codes 0.42 ms
+// interleaved and 0.43 by halves, 5.4 to 5.6 TB/s.  In binary32 by halves 1.13 ms, 5.5 TB/s, to codes
+// 0.70 ms; interleaved to codes 0.72 ms, but to binary32 1.75 ms, 3.5 TB/s: a lane's two runs of 16
+// bytes then lie side by side, so that each store instruction writes every other 16 bytes past the
+// caches, and the memory is written 1.6 times.  57344 x (24 + 24) x 128 bf16 to codes 0.194 ms, 5.4
+// TB/s; 32768 x (32 + 8) x 128 by halves 0.117 ms, 5.7 TB/s, to codes 0.099.
 #include <type_traits>
 
 #include "mxq_int8.hpp"
@@ -334,7 +338,8 @@ hipError_t launch_qk_norm_rope(const QkNormParams& args, bool f32, bool quant, b
   // 75600 x (40 + 40) x 128; four: 0.55 ms too, but 0.20 for 0.185 ms where 24 heads leave
   // half of them idle at the end).  Where the queries and keys of a token are no more than two
   // sets, (token, head) pairs: 30000 tokens x (2 + 2) heads x 128 28 -> 16 us, (1 + 1) 23 -> 9,
-  // (4 + 4) 32 -> 30, but (8 + 8) 41 and 56.
+  // (4 + 4) 32 -> 30, but (8 + 8) 41 and 56 (from the memory-side cache; not from it, 25000 x (1 + 1)
+  // takes 9.3 us, 30000 x (2 + 2) 18, (4 + 4) 32, (8 + 8) 43).
   auto u = [&](auto g, auto f, auto q, auto h) {
     const int heads = args.q.heads + args.k.heads;
     if (args.tokens < 512)

@@ -22,7 +22,8 @@ constexpr int kFewTokens = 8;                // up to so many tokens the tiles a
 //   2048 x 5120 x 5120: 57, 78, 79, 99, 102;  128 x 5120 x 5120: 60, 43, 29, 22, 15.5
 //   64 x 13824 x 5120: 64 x 32 27.5, 64 x 64 36, 64 x 64 in 3 parts of K 20.6
 // off_lines: factor on per_window where K is no multiple of a cache line, so that contiguous rows
-// start off the lines.
+// start off the lines.  The plan knows no bases or pitches (the workspace has a size for M, N and K
+// alone), so rows off the lines for another reason are counted as if on them; shifted() goes by them.
 struct TileCost {
   int bm, bn;
   float fixed, per_window, again, off_lines;
