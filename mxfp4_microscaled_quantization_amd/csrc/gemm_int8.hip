@@ -24,7 +24,7 @@
 //    fragment read takes its chunk from block w or w + 1, which the ring holds both (pitches
 //    are multiples of 16, so that a row's offset in its line is the same every 8 rows).
 //
-// What bounds it: power on large shapes.  75600 x 5120 x 13824 takes 3.93 to 3.95 ms on codes of
+// What bounds it: power on large shapes.  75600 x 5120 x 13824 takes 3.92 to 3.95 ms on codes of
 // normal values, 4.05 ms on uniform ones, and 3.75 to 4.18 ms over all GPUs and profiled runs (2.56 to
 // 2.86 POP/s), with the matrix cores 75 % busy; the same MFMAs from registers alone run at 3.87
 // POP/s on such codes.  Where each CU has a tile or two, the latencies at a tile's ends and the 64
