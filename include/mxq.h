@@ -442,6 +442,135 @@ mxq_status mxq_quantize_qk_norm_rope(const void* q, int64_t heads_q, int64_t ld_
                                      void* stream);
 
 /*
+ * Layer norm, and activations kept in 8 bits for the backward pass: what stands between the
+ * 8-bit products of a transformer block, forward and backward.  The codes and row scales are
+ * those of mxq_quantize_int8.
+ *
+ * mxq_layer_norm -- for each row x of cols elements, in binary32:
+ *   mean = sum x / cols;  rstd = 1 / sqrt( sum (x - mean)^2 / cols + eps );
+ *   y = (x - mean) * rstd * w + b,  rounded to `dt` once.
+ * The deviations are taken from the mean itself (no difference of two squares).  A row with an
+ * infinity or a NaN comes out as NaN; a row whose squares overflow binary32 (deviations of
+ * 2^60 and more) as b, infinities or NaN; with eps == 0 a row of equal values as NaN.  Other
+ * rows are unaffected.
+ * x       : rows x cols of `dt`, pitch ld_x elements; base and pitch 16-byte aligned.
+ * w, b    : cols weights and biases of w_dt, 16-byte aligned; either may be NULL (1, 0).
+ * y       : out, rows x cols of `dt`, pitch ld_y elements; base and pitch 16-byte aligned.  May be
+ *           x with the same pitch; no other overlap.
+ * mean, rstd : out, float[rows] each, or both NULL.
+ * x_codes, x_scales : out, the checkpoint mxq_quantize_int8(x), bit for bit (pitch ld_xc bytes, base
+ *           and pitch multiples of 16), or x_codes NULL for none (ld_xc and x_scales are then ignored).
+ * cols    : a multiple of 8 (16 with x_codes), 8 to 16384.  eps finite and >= 0.
+ */
+mxq_status mxq_layer_norm(const void* x, mxq_dtype dt, int64_t rows, int64_t cols, int64_t ld_x, const void* w,
+                          const void* b, mxq_dtype w_dt, float eps, void* y, int64_t ld_y, float* mean,
+                          float* rstd, int8_t* x_codes, int64_t ld_xc, float* x_scales, void* stream);
+
+/*
+ * mxq_quantize_layer_norm -- the same, then the rule of mxq_quantize_int8 on the binary32 values of
+ * each row: codes (pitch ld_codes bytes; base and pitch multiples of 16) and float scales[rows],
+ * operands of mxq_gemm_w8a8.  cols: a multiple of 16.
+ */
+mxq_status mxq_quantize_layer_norm(const void* x, mxq_dtype dt, int64_t rows, int64_t cols, int64_t ld_x,
+                                   const void* w, const void* b, mxq_dtype w_dt, float eps, int8_t* codes,
+                                   int64_t ld_codes, float* scales, float* mean, float* rstd, int8_t* x_codes,
+                                   int64_t ld_xc, float* x_scales, void* stream);
+
+/*
+ * mxq_layer_norm_backward -- with xh = (x - mean) * rstd and g = dy * w, in binary32:
+ *   dx = rstd * ( g - sum g / cols - xh * sum (g xh) / cols ), rounded to `dt` once;
+ *   dw = sum over rows of dy * xh;  db = sum over rows of dy.
+ * The sums over rows are formed in an order that rows and cols alone decide: the same inputs
+ * give the same bits.
+ * dy, dx  : rows x cols of `dt`; dx may be dy with the same pitch.
+ * x       : with x_scales NULL the kept input, of `dt`; else its codes (int8, one float x_scales
+ *           for each row; cols a multiple of 16), which stand for fl32(code * scale).
+ * All bases and pitches 16-byte aligned.
+ * mean, rstd : float[rows], as mxq_layer_norm left them.
+ * w       : cols weights of w_dt, or NULL for 1.
+ * dw, db  : out, float[cols] each, 16-byte aligned, or both NULL.  rows == 0 writes zeros.
+ * workspace, ws_bytes : device memory of at least mxq_layer_norm_backward_workspace_bytes(rows, cols)
+ *           bytes, 16-byte aligned (NULL where that is 0, or without dw and db), owned by the caller and
+ *           not used by anything else until the call's work on `stream` is done.
+ */
+mxq_status mxq_layer_norm_backward(const void* dy, mxq_dtype dt, int64_t rows, int64_t cols, int64_t ld_dy,
+                                   const void* x, int64_t ld_x, const float* x_scales, const float* mean,
+                                   const float* rstd, const void* w, mxq_dtype w_dt, void* dx, int64_t ld_dx,
+                                   float* dw, float* db, void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace of mxq_layer_norm_backward with dw and db (0 for an empty or invalid shape).  Host only. */
+size_t mxq_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+
+/* Activation functions of a feed-forward layer (mxq_activation), s(z) = 1 / (1 + exp(-z)). */
+typedef enum {
+  MXQ_ACT_GELU_TANH = 0, /* u * s(2 sqrt(2 / pi) (u + 0.044715 u^3)): the tanh form of GELU */
+  MXQ_ACT_SILU = 1,      /* u * s(u) */
+  MXQ_ACTIVATION_MAX_ENUM = 0x7FFFFFFF
+} mxq_activation_kind;
+
+/*
+ * mxq_activation -- y = f(u) element by element, in binary32, rounded to `dt` once, with an 8-bit
+ * checkpoint of u for the backward pass.
+ * u       : rows x cols of `dt`, pitch ld_u elements; base and pitch 16-byte aligned.
+ * y       : out, rows x cols of `dt`, pitch ld_y elements; base and pitch 16-byte aligned.  May be u
+ *           with the same pitch; no other overlap.
+ * u_codes, u_scales : out, the checkpoint (pitch ld_uc bytes; base and pitch multiples of 16), or
+ *           u_codes NULL for none (ld_uc and u_scales are then ignored).  It is the rule of
+ *           mxq_quantize_int8 on u clamped to [-L, L], L = 4 for MXQ_ACT_GELU_TANH and 8 for MXQ_ACT_SILU:
+ *           beyond L the derivative is within 4e-4 and 3e-3 of 0 or 1, and the step stays at most
+ *           L / 127.  Infinities are clamped; a row with a NaN gets scale NaN and codes 0.
+ * f(+inf) = +inf, f(-inf) = NaN.
+ * cols    : a multiple of 8 (16 with u_codes), up to 65536.
+ */
+mxq_status mxq_activation(const void* u, mxq_dtype dt, int64_t rows, int64_t cols, int64_t ld_u,
+                          mxq_activation_kind act, void* y, int64_t ld_y, int8_t* u_codes, int64_t ld_uc,
+                          float* u_scales, void* stream);
+
+/*
+ * mxq_quantize_activation -- the same, then the rule of mxq_quantize_int8 on the binary32 values
+ * of each row: codes (pitch ld_codes bytes; base and pitch multiples of 16) and float scales[rows],
+ * operands of mxq_gemm_w8a8.  cols: a multiple of 16.
+ */
+mxq_status mxq_quantize_activation(const void* u, mxq_dtype dt, int64_t rows, int64_t cols, int64_t ld_u,
+                                   mxq_activation_kind act, int8_t* codes, int64_t ld_codes, float* scales,
+                                   int8_t* u_codes, int64_t ld_uc, float* u_scales, void* stream);
+
+/*
+ * mxq_activation_backward -- du = dy * f'(v) with v = fl32(code * scale) of the checkpoint, in
+ * binary32, rounded to `dt` once.
+ * dy, du  : rows x cols of `dt`, pitches in elements, 16-byte aligned; du may be dy with the same pitch.
+ * u_codes, u_scales : the checkpoint of the same activation.  cols: a multiple of 16.
+ */
+mxq_status mxq_activation_backward(const void* dy, mxq_dtype dt, int64_t rows, int64_t cols, int64_t ld_dy,
+                                   const int8_t* u_codes, int64_t ld_uc, const float* u_scales,
+                                   mxq_activation_kind act, void* du, int64_t ld_du, void* stream);
+
+/*
+ * mxq_grad_weight_int8 -- the weight gradient of mxq_gemm_w8a8 from the codes that the forward
+ * product took, N x K as the weights are:
+ *   dW[n,k] = sum_m dy[m,n] * bf16_RNE( fl32( code[m,k] * scale[m] ) ), binary32 accumulation over
+ * the values that mxq_dequantize_int8 gives, rounded to out_dt once; with `accumulate` not 0 that
+ * sum is added to what `out` holds, in binary32, before the rounding.
+ * The order of the sum is decided by M, N and K alone: the same inputs give the same bits.
+ * dy      : M x N bf16, pitch ld_dy elements below 2^23; base and pitch 16-byte aligned.
+ * codes   : M x K int8, pitch ld_codes bytes; base and pitch multiples of 16.  scales : float[M].
+ * out     : N x K of out_dt, pitch ld_out elements (>= K), naturally aligned (stored fastest on 16-byte
+ *           boundaries).
+ * N % 8 == 0, K % 16 == 0; N and K up to 2^22, N * K up to 2^36, M * K below 2^35.  M == 0 gives zeros
+ * (with accumulate: leaves `out`).
+ * workspace, ws_bytes : device memory of at least mxq_grad_weight_int8_workspace_bytes(M, N, K)
+ *           bytes, 16-byte aligned (NULL where that is 0), owned by the caller and not used by anything
+ *           else until the call's work on `stream` is done.
+ */
+mxq_status mxq_grad_weight_int8(const uint16_t* dy, int64_t ld_dy, const int8_t* codes, int64_t ld_codes,
+                                const float* scales, int64_t M, int64_t N, int64_t K, void* out,
+                                mxq_dtype out_dt, int64_t ld_out, int accumulate, void* workspace,
+                                size_t ws_bytes, void* stream);
+
+/* Workspace of mxq_grad_weight_int8 for a shape (0 for an empty or invalid one).  Host only. */
+size_t mxq_grad_weight_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/*
  * Measurement aid (not part of the quantize / GEMM path).
  *
  * mxq_mfma_ceiling -- the MFMA throughput the chip sustains on the operand bits of a GEMM

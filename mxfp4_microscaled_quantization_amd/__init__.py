@@ -10,7 +10,8 @@ built (``python mxfp4_microscaled_quantization_amd/build.py``); there is no fall
 Function names mirror the C entry points without the ``mxq_`` prefix:
 ``quantize``, ``quantize_fp8``, ``absmax``, ``gemm_w4a4``, ``gemm_w4a4_fused``, ``gemm_w4a8``, ``gemm_bf16``,
 ``sqnr``, ``dequantize``, ``dequantize_fp8``, ``fp8_static_scales``, ``quantize_int8``, ``dequantize_int8``, ``gemm_w8a8``,
-``gemm_w8a8_fused``, ``qk_norm_rope``, ``quantize_qk_norm_rope``.  ``lib`` exposes the raw ctypes functions.
+``gemm_w8a8_fused``, ``qk_norm_rope``, ``quantize_qk_norm_rope``, ``layer_norm``, ``quantize_layer_norm``,
+``layer_norm_backward``, ``activation``, ``quantize_activation``, ``activation_backward``, ``grad_weight_int8``.  ``lib`` exposes the raw ctypes functions.
 """
 
 import ctypes
@@ -23,7 +24,8 @@ __all__ = [
     "gemm_w4a4", "gemm_w4a4_fused", "gemm_w4a8", "gemm_bf16", "sqnr", "sqnr_noalloc", "sqnr_workspace_bytes", "dequantize", "dequantize_fp8",
     "quantize_int8", "dequantize_int8", "gemm_w8a8", "gemm_w8a8_fused", "w8a8_workspace_bytes",
     "w8a8_fused_workspace_bytes",
-    "qk_norm_rope", "quantize_qk_norm_rope", "ROPE_STYLES", "mfma_ceiling", "MFMA_FLOP", "check_buffer",
+    "qk_norm_rope", "quantize_qk_norm_rope", "ROPE_STYLES", "layer_norm", "quantize_layer_norm", "layer_norm_backward",
+    "activation", "quantize_activation", "activation_backward", "ACTIVATIONS", "grad_weight_int8", "mfma_ceiling", "MFMA_FLOP", "check_buffer",
     "LIB_PATH", "ABI_SYMBOLS", "ABI_VERSION",
 ]
 
@@ -42,6 +44,9 @@ _QK_ARGS = [_ptr, _i64, _i64, _i64, _ptr, _i64, _i64, _i64, ctypes.c_int, _i64, 
             _ptr, _ptr, _i64, _i64, _i64, _ptr, ctypes.c_int]
 
 #: every exported symbol with (restype, argtypes) -- the C ABI of include/mxq.h
+_NORM_ARGS = [_ptr, ctypes.c_int, _i64, _i64, _i64, _ptr, _ptr, ctypes.c_int, _f32]
+_NORM_SAVED = [_ptr, _ptr, _ptr, _i64, _ptr]
+
 ABI_SYMBOLS = {
     "mxq_quantize": (ctypes.c_int, [_ptr, ctypes.c_int, _i64, _i64, _i64, _ptr, _i64, _ptr, _i64, _ptr]),
     "mxq_quantize_rule": (ctypes.c_int, [_ptr, ctypes.c_int, _i64, _i64, _i64, _ptr, _i64, _ptr, _i64, ctypes.c_int,
@@ -74,6 +79,20 @@ ABI_SYMBOLS = {
     "mxq_gemm_w8a8_fused_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "mxq_qk_norm_rope": (ctypes.c_int, _QK_ARGS + [_ptr, _i64, _i64, _ptr, _i64, _i64, _ptr]),
     "mxq_quantize_qk_norm_rope": (ctypes.c_int, _QK_ARGS + [_ptr, _i64, _i64, _ptr, _i64] * 2 + [_ptr]),
+    "mxq_layer_norm": (ctypes.c_int, _NORM_ARGS + [_ptr, _i64] + _NORM_SAVED + [_ptr]),
+    "mxq_quantize_layer_norm": (ctypes.c_int, _NORM_ARGS + [_ptr, _i64, _ptr] + _NORM_SAVED + [_ptr]),
+    "mxq_layer_norm_backward_workspace_bytes": (_sz, [_i64, _i64]),
+    "mxq_layer_norm_backward": (ctypes.c_int, [_ptr, ctypes.c_int, _i64, _i64, _i64, _ptr, _i64, _ptr, _ptr, _ptr, _ptr,
+                                               ctypes.c_int, _ptr, _i64, _ptr, _ptr, _ptr, _sz, _ptr]),
+    "mxq_activation": (ctypes.c_int, [_ptr, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _ptr, _i64, _ptr, _i64, _ptr,
+                                      _ptr]),
+    "mxq_quantize_activation": (ctypes.c_int, [_ptr, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _ptr, _i64, _ptr, _ptr,
+                                               _i64, _ptr, _ptr]),
+    "mxq_activation_backward": (ctypes.c_int, [_ptr, ctypes.c_int, _i64, _i64, _i64, _ptr, _i64, _ptr, ctypes.c_int, _ptr,
+                                               _i64, _ptr]),
+    "mxq_grad_weight_int8": (ctypes.c_int, [_ptr, _i64, _ptr, _i64, _ptr, _i64, _i64, _i64, _ptr, ctypes.c_int, _i64,
+                                            ctypes.c_int, _ptr, _sz, _ptr]),
+    "mxq_grad_weight_int8_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "mxq_last_error": (ctypes.c_char_p, []),
     "mxq_abi_version": (ctypes.c_int, []),
 }
@@ -712,3 +731,174 @@ def quantize_qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions=None, ep
     _call(lib.mxq_quantize_qk_norm_rope, q.device, *args, qc.data_ptr(), Hq * D, D, qs.data_ptr(), Hq,
           kc.data_ptr(), Hk * D, D, ks.data_ptr(), Hk)
     return qc, qs, kc, ks
+
+
+# ---------------------------------------------------------------------------------
+# Layer norm, and activations kept in 8 bits for the backward pass.  Forward and backward are separate
+# calls, and nothing is recorded for autograd here either.
+
+_SAVES = (None, "x", "int8")
+
+
+def _plane(t, name, dtype, rows, cols, device):
+    """A given [rows, cols] output, or a new one: (tensor, row pitch)."""
+    if t is None:
+        return _empty((rows, cols), (cols, 1), dtype=dtype, device=device), cols
+    return t, _matrix(t, name, dtype, device, (rows, cols))
+
+
+def _row_values(rows, device):
+    return _empty((rows,), (1,), dtype=torch.float32, device=device)
+
+
+def _norm_vectors(weight, bias, cols, device):
+    """The addresses of the weights and biases and their dtype code."""
+    dt = None
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _there(t, name, device)
+            dtype = t.dtype
+            if dtype not in _FLOATS:
+                raise ValueError(f"{name} must be bfloat16 or float32")
+            if t.shape != (cols,) or (cols > 1 and t.stride(0) != 1):
+                raise ValueError(f"{name} must be contiguous, of shape ({cols},) (got {tuple(t.shape)})")
+            if dt is not None and dtype != dt:
+                raise ValueError("weight and bias must have one dtype")
+            dt = dtype
+    return _opt(weight), _opt(bias), MXQ_BF16 if dt == torch.bfloat16 else MXQ_F32
+
+
+def _checkpoint(rows, cols, device):
+    """New codes and scales: (tensors, C arguments)."""
+    codes, scales = _empty((rows, cols), (cols, 1), dtype=torch.int8, device=device), _row_values(rows, device)
+    return (codes, scales), (codes.data_ptr(), cols, scales.data_ptr())
+
+
+def _norm_inputs(x, weight, bias, eps, save):
+    if save not in _SAVES:
+        raise ValueError(f"save must be one of {_SAVES}")
+    ld = _matrix(x, "x", _FLOATS)
+    dev, (R, C) = x.device, x.shape
+    args = (x.data_ptr(), _dtype_code(x), R, C, ld, *_norm_vectors(weight, bias, C, dev), eps)
+    if save is None:
+        return args, (), (None, None, None, 0, None)
+    mean, rstd = _row_values(R, dev), _row_values(R, dev)
+    kept, kept_args = _checkpoint(R, C, dev) if save == "int8" else ((), (None, 0, None))
+    return args, (mean, rstd, *kept), (mean.data_ptr(), rstd.data_ptr(), *kept_args)
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-6, save=None, out=None):
+    """Layer norm of the rows of ``x`` [T, C] (bf16 or fp32; C a multiple of 8 up to 16384): ``y`` of x's type.
+
+    ``weight``, ``bias``: [C], bf16 or fp32, either None.  ``save``: what the backward pass needs, from the same
+    pass over x: "x" returns (y, mean, rstd), to be kept with x itself; "int8" (C a multiple of 16) returns
+    (y, mean, rstd, x_codes, x_scales), the last two equal to quantize_int8(x).  ``out=x`` works in place."""
+    args, saved, saved_args = _norm_inputs(x, weight, bias, eps, save)
+    y, ld = _plane(out, "out", x.dtype, *x.shape, x.device)
+    _call(lib.mxq_layer_norm, x.device, *args, y.data_ptr(), ld, *saved_args)
+    return (y, *saved) if saved else y
+
+
+def quantize_layer_norm(x, weight=None, bias=None, eps=1e-6, save=None):
+    """layer_norm to 8-bit codes by the rule of quantize_int8, operands of gemm_w8a8: (codes int8 [T, C], scales
+    float32 [T]), followed by what ``save`` asks for as in layer_norm.  C a multiple of 16."""
+    args, saved, saved_args = _norm_inputs(x, weight, bias, eps, save)
+    (codes, scales), _ = _checkpoint(*x.shape, x.device)
+    _call(lib.mxq_quantize_layer_norm, x.device, *args, codes.data_ptr(), x.shape[1], scales.data_ptr(), *saved_args)
+    return (codes, scales, *saved)
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, x_scales=None, out=None):
+    """Gradient of layer_norm: (dx, dweight, dbias), the last two float32 [C] and None without ``weight``.
+
+    ``dy`` [T, C], bf16 or fp32; ``x``: the forward input, of dy's type, or its int8 codes with ``x_scales``
+    (save="int8").  ``mean``, ``rstd``: float32 [T] of the forward pass.  dx has dy's type; ``out=dy`` works in place.
+    The sums over rows are formed in a fixed order."""
+    ld = _matrix(dy, "dy", _FLOATS)
+    dev, (R, C) = dy.device, dy.shape
+    if x_scales is not None:
+        _flat(x_scales, "x_scales", R, dev)
+    ldx = _matrix(x, "x", dy.dtype if x_scales is None else torch.int8, dev, (R, C))
+    _flat(mean, "mean", R, dev)
+    _flat(rstd, "rstd", R, dev)
+    w, _, w_dt = _norm_vectors(weight, None, C, dev)
+    dx, ldo = _plane(out, "out", dy.dtype, R, C, dev)
+    dw = db = ws = None
+    nbytes = 0
+    if weight is not None:
+        dw, db = _row_values(C, dev), _row_values(C, dev)
+        nbytes = lib.mxq_layer_norm_backward_workspace_bytes(R, C)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    _call(lib.mxq_layer_norm_backward, dev, dy.data_ptr(), _dtype_code(dy), R, C, ld, x.data_ptr(), ldx, _opt(x_scales),
+          mean.data_ptr(), rstd.data_ptr(), w, w_dt, dx.data_ptr(), ldo, _opt(dw), _opt(db), _opt(ws), nbytes)
+    return dx, dw, db
+
+
+ACTIVATIONS = {"gelu_tanh": 0, "silu": 1}
+
+
+def _act_code(act):
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
+    return ACTIVATIONS[act]
+
+
+def _act_inputs(u, act, save):
+    if save not in (None, "int8"):
+        raise ValueError("save must be None or 'int8'")
+    ld = _matrix(u, "u", _FLOATS)
+    R, C = u.shape
+    kept, kept_args = _checkpoint(R, C, u.device) if save else ((), (None, 0, None))
+    return (u.data_ptr(), _dtype_code(u), R, C, ld, _act_code(act)), kept, kept_args
+
+
+def activation(u, act="gelu_tanh", save=None, out=None):
+    """f(u) of a feed-forward layer, element by element ([T, C], bf16 or fp32, C a multiple of 8 up to 65536): ``y`` of u's
+    type.  ``act``: "gelu_tanh" or "silu".  save="int8" (C a multiple of 16) returns (y, u_codes, u_scales), the 8-bit
+    checkpoint that activation_backward takes, from the same pass.  ``out=u`` works in place."""
+    args, kept, kept_args = _act_inputs(u, act, save)
+    y, ld = _plane(out, "out", u.dtype, *u.shape, u.device)
+    _call(lib.mxq_activation, u.device, *args, y.data_ptr(), ld, *kept_args)
+    return (y, *kept) if kept else y
+
+
+def quantize_activation(u, act="gelu_tanh", save=None):
+    """activation to 8-bit codes by the rule of quantize_int8, operands of gemm_w8a8: (codes int8 [T, C], scales
+    float32 [T]), followed by the checkpoint with save="int8".  C a multiple of 16."""
+    args, kept, kept_args = _act_inputs(u, act, save)
+    (codes, scales), _ = _checkpoint(*u.shape, u.device)
+    _call(lib.mxq_quantize_activation, u.device, *args, codes.data_ptr(), u.shape[1], scales.data_ptr(), *kept_args)
+    return (codes, scales, *kept)
+
+
+def activation_backward(dy, u_codes, u_scales, act="gelu_tanh", out=None):
+    """dy * f'(u) from the 8-bit checkpoint of the same ``act``: [T, C] of dy's type (``out=dy`` works in place)."""
+    ld = _matrix(dy, "dy", _FLOATS)
+    dev, (R, C) = dy.device, dy.shape
+    ldc = _matrix(u_codes, "u_codes", torch.int8, dev, (R, C))
+    _flat(u_scales, "u_scales", R, dev)
+    du, ldo = _plane(out, "out", dy.dtype, R, C, dev)
+    _call(lib.mxq_activation_backward, dev, dy.data_ptr(), _dtype_code(dy), R, C, ld, u_codes.data_ptr(), ldc,
+          u_scales.data_ptr(), _act_code(act), du.data_ptr(), ldo)
+    return du
+
+
+def grad_weight_int8(dy, codes, scales, out=None, out_dtype=torch.float32, accumulate=False):
+    """Weight gradient of gemm_w8a8 from the activations' codes: dy [M, N] (bf16)^T x dequantize_int8(codes [M, K],
+    scales [M]) -> [N, K], float32 or bfloat16 (``out`` decides where it is given).  N a multiple of 8, K of 16; rows
+    may be strided.  accumulate=True adds to ``out``.  The sum over M is formed in an order that the sizes alone decide."""
+    ldy = _matrix(dy, "dy", torch.bfloat16)
+    dev, (M, N) = dy.device, dy.shape
+    ldc = _matrix(codes, "codes", torch.int8, dev)
+    K = codes.shape[1]
+    if codes.shape[0] != M:
+        raise ValueError(f"codes must have {M} rows (got {codes.shape[0]})")
+    _flat(scales, "scales", M, dev)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    out, ld = _w8_out(N, K, dev, out, out_dtype)
+    nbytes = lib.mxq_grad_weight_int8_workspace_bytes(M, N, K)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    _call(lib.mxq_grad_weight_int8, dev, dy.data_ptr(), ldy, codes.data_ptr(), ldc, scales.data_ptr(), M, N, K,
+          out.data_ptr(), _dtype_code(out), ld, int(accumulate), _opt(ws), nbytes)
+    return out

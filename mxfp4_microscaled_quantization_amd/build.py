@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libmxq.so")
 ARCH = "gfx950"
 
 SOURCES = ["mxq_api.hip", "quantize.hip", "hadamard.hip", "gemm.hip", "gemm_scaled.hip", "sqnr.hip", "ceiling.hip",
-           "int8.hip", "gemm_int8.hip", "qk_norm.hip"]
+           "int8.hip", "gemm_int8.hip", "qk_norm.hip", "layer_norm.hip", "activation.hip", "grad_weight.hip"]
 # per-source compiler options (see the comment at the top of each source)
 SOURCE_FLAGS = {"gemm_scaled.hip": ["-mllvm", "-disable-machine-sink"], "hadamard.hip": ["-fno-slp-vectorize"]}
 

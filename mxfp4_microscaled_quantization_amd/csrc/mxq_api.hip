@@ -261,6 +261,114 @@ mxq_status qk_norm_rope(const char* fn, HeadArgs q, HeadArgs k, mxq_dtype dt, in
   return hip_status(fn, mxq::launch_qk_norm_rope(p, dt == MXQ_F32, quant, style == MXQ_ROPE_HALVES, stream));
 }
 
+// A rows x cols plane of elements of `bytes` besides the input: pitch, and where it is not empty,
+// pointer and alignment.
+mxq_status check_plane(const char* fn, const char* name, const void* ptr, int64_t rows, int64_t cols, int64_t ld,
+                       int64_t bytes, int64_t align) {
+  if (ld < cols) return fail(MXQ_ERR_INVALID_ARG, "%s: ld of %s (%lld) < cols (%lld)", fn, name, (long long)ld, (long long)cols);
+  if (!pitch_ok(ld)) return fail(MXQ_ERR_INVALID_ARG, "%s: ld of %s (%lld) must be below 2^32", fn, name, (long long)ld);
+  if (rows > 0 && cols > 0) {
+    if (!ptr) return fail(MXQ_ERR_INVALID_ARG, "%s: %s is NULL", fn, name);
+    if (!aligned(ptr, (uintptr_t)align) || ld * bytes % align != 0)
+      return fail(MXQ_ERR_INVALID_ARG, "%s: %s base and row pitch must be %lld-byte aligned", fn, name, (long long)align);
+  }
+  return MXQ_OK;
+}
+
+// A float for each row, or none where `may_be_null`.
+mxq_status check_row_values(const char* fn, const char* name, const float* ptr, int64_t rows, bool may_be_null) {
+  if (rows > 0 && ((!ptr && !may_be_null) || !aligned(ptr, 4)))
+    return fail(MXQ_ERR_INVALID_ARG, "%s: %s must be a %s4-byte aligned pointer", fn, name, may_be_null ? "" : "non-NULL ");
+  return MXQ_OK;
+}
+
+mxq_status check_norm(const char* fn, int64_t cols, const void* w, const void* b, mxq_dtype w_dt) {
+  if (dtype_bytes(w_dt) == 0) return fail(MXQ_ERR_UNSUPPORTED, "%s: unknown dtype %d", fn, (int)w_dt);
+  if (cols < 8 || cols > mxq::kNormMaxCols)
+    return fail(MXQ_ERR_INVALID_ARG, "%s: cols (%lld) must be 8 to %lld", fn, (long long)cols, (long long)mxq::kNormMaxCols);
+  if (!aligned(w, 16) || !aligned(b, 16)) return fail(MXQ_ERR_INVALID_ARG, "%s: w and b must be 16-byte aligned", fn);
+  return MXQ_OK;
+}
+
+mxq_status layer_norm(const char* fn, const void* x, mxq_dtype dt, int64_t rows, int64_t cols, int64_t ld_x,
+                      const void* w, const void* b, mxq_dtype w_dt, float eps, void* y, int64_t ld_y, float* scales,
+                      float* mean, float* rstd, int8_t* x_codes, int64_t ld_xc, float* x_scales, bool quant,
+                      hipStream_t stream) {
+  mxq_status st = check_input(fn, x, dt, rows, cols, ld_x, quant || x_codes ? 16 : 8);
+  if (st != MXQ_OK) return st;
+  if ((st = check_norm(fn, cols, w, b, w_dt)) != MXQ_OK) return st;
+  if (!(eps >= 0.0f) || !(eps < __builtin_inff())) return fail(MXQ_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", fn);
+  if ((st = check_plane(fn, quant ? "codes" : "y", y, rows, cols, ld_y, quant ? 1 : dtype_bytes(dt), 16)) != MXQ_OK) return st;
+  if (quant && (st = check_row_values(fn, "scales", scales, rows, false)) != MXQ_OK) return st;
+  if (!mean != !rstd) return fail(MXQ_ERR_INVALID_ARG, "%s: mean and rstd must be given together", fn);
+  if ((st = check_row_values(fn, "mean", mean, rows, true)) != MXQ_OK) return st;
+  if ((st = check_row_values(fn, "rstd", rstd, rows, true)) != MXQ_OK) return st;
+  if (x_codes) {
+    if ((st = check_plane(fn, "x_codes", x_codes, rows, cols, ld_xc, 1, 16)) != MXQ_OK) return st;
+    if ((st = check_row_values(fn, "x_scales", x_scales, rows, false)) != MXQ_OK) return st;
+  }
+  mxq::NormParams p;
+  p.x = x;
+  p.w = w;
+  p.b = b;
+  p.y = y;
+  p.scales = scales;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.kept = x_codes;
+  p.kept_scales = x_scales;
+  p.rows = rows;
+  p.ld_x = ld_x;
+  p.ld_y = ld_y;
+  p.ld_kept = ld_xc;
+  p.units = (uint32_t)(cols / 8);
+  p.w_f32 = w_dt == MXQ_F32 ? 1 : 0;
+  p.eps = eps;
+  p.inv_cols = 1.0f / (float)cols;
+  return hip_status(fn, mxq::launch_layer_norm(p, dt == MXQ_F32, quant, stream));
+}
+
+mxq_status check_act(const char* fn, mxq_activation_kind act) {
+  if (act != MXQ_ACT_GELU_TANH && act != MXQ_ACT_SILU)
+    return fail(MXQ_ERR_UNSUPPORTED, "%s: unknown activation %d", fn, (int)act);
+  return MXQ_OK;
+}
+
+mxq_status activation(const char* fn, const void* u, mxq_dtype dt, int64_t rows, int64_t cols, int64_t ld_u,
+                      mxq_activation_kind act, void* y, int64_t ld_y, float* scales, int8_t* u_codes, int64_t ld_uc,
+                      float* u_scales, bool quant, hipStream_t stream) {
+  mxq_status st = check_act(fn, act);
+  if (st != MXQ_OK) return st;
+  if ((st = check_input(fn, u, dt, rows, cols, ld_u, quant || u_codes ? 16 : 8)) != MXQ_OK) return st;
+  if (cols > mxq::kActMaxCols)
+    return fail(MXQ_ERR_INVALID_ARG, "%s: cols (%lld) must be at most %lld", fn, (long long)cols, (long long)mxq::kActMaxCols);
+  if ((st = check_plane(fn, quant ? "codes" : "y", y, rows, cols, ld_y, quant ? 1 : dtype_bytes(dt), 16)) != MXQ_OK) return st;
+  if (quant && (st = check_row_values(fn, "scales", scales, rows, false)) != MXQ_OK) return st;
+  if (u_codes) {
+    if ((st = check_plane(fn, "u_codes", u_codes, rows, cols, ld_uc, 1, 16)) != MXQ_OK) return st;
+    if ((st = check_row_values(fn, "u_scales", u_scales, rows, false)) != MXQ_OK) return st;
+  }
+  mxq::ActParams p;
+  p.u = u;
+  p.y = y;
+  p.scales = scales;
+  p.kept = u_codes;
+  p.kept_scales = u_scales;
+  p.rows = rows;
+  p.ld_u = ld_u;
+  p.ld_y = ld_y;
+  p.ld_kept = ld_uc;
+  p.units = (uint32_t)(cols / 8);
+  return hip_status(fn, mxq::launch_activation(p, dt == MXQ_F32, quant,
+                                               act == MXQ_ACT_GELU_TANH ? mxq::ACT_GELU_TANH : mxq::ACT_SILU, stream));
+}
+
+// Shapes of which the weight gradient has a plan.
+bool grad_shape_ok(int64_t M, int64_t N, int64_t K) {
+  return M >= 0 && N > 0 && K > 0 && N % 8 == 0 && K % 16 == 0 && M <= kMaxDim - 256 && N <= ((int64_t)1 << 22) &&
+         K <= ((int64_t)1 << 22) && N * K <= ((int64_t)1 << 36) && M * (K / 8) < ((int64_t)1 << 32);
+}
+
 hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 
 }  // namespace
@@ -698,6 +806,132 @@ mxq_status mxq_quantize_qk_norm_rope(const void* q, int64_t heads_q, int64_t ld_
                       HeadArgs{"k", k, heads_k, ld_k, hs_k, w_k, codes_k, ld_ck, hs_ck, scales_k, ld_sk}, dt, tokens,
                       head_dim, w_dt, eps, cos, sin, ld_table, table_rows, rot_dim, positions, style, true,
                       as_stream(stream));
+}
+
+mxq_status mxq_layer_norm(const void* x, mxq_dtype dt, int64_t rows, int64_t cols, int64_t ld_x, const void* w,
+                          const void* b, mxq_dtype w_dt, float eps, void* y, int64_t ld_y, float* mean, float* rstd,
+                          int8_t* x_codes, int64_t ld_xc, float* x_scales, void* stream) {
+  return layer_norm("mxq_layer_norm", x, dt, rows, cols, ld_x, w, b, w_dt, eps, y, ld_y, nullptr, mean, rstd, x_codes,
+                    ld_xc, x_scales, false, as_stream(stream));
+}
+
+mxq_status mxq_quantize_layer_norm(const void* x, mxq_dtype dt, int64_t rows, int64_t cols, int64_t ld_x, const void* w,
+                                   const void* b, mxq_dtype w_dt, float eps, int8_t* codes, int64_t ld_codes,
+                                   float* scales, float* mean, float* rstd, int8_t* x_codes, int64_t ld_xc,
+                                   float* x_scales, void* stream) {
+  return layer_norm("mxq_quantize_layer_norm", x, dt, rows, cols, ld_x, w, b, w_dt, eps, codes, ld_codes, scales, mean,
+                    rstd, x_codes, ld_xc, x_scales, true, as_stream(stream));
+}
+
+size_t mxq_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
+  if (rows <= 0 || rows > kMaxDim || cols < 8 || cols > mxq::kNormMaxCols || cols % 8 != 0) return 0;
+  return mxq::layer_norm_backward_workspace_bytes(rows, cols);
+}
+
+mxq_status mxq_layer_norm_backward(const void* dy, mxq_dtype dt, int64_t rows, int64_t cols, int64_t ld_dy,
+                                   const void* x, int64_t ld_x, const float* x_scales, const float* mean,
+                                   const float* rstd, const void* w, mxq_dtype w_dt, void* dx, int64_t ld_dx, float* dw,
+                                   float* db, void* workspace, size_t ws_bytes, void* stream) {
+  const char* fn = "mxq_layer_norm_backward";
+  const bool codes = x_scales != nullptr;
+  mxq_status st = check_input(fn, dy, dt, rows, cols, ld_dy, codes ? 16 : 8);
+  if (st != MXQ_OK) return st;
+  if ((st = check_norm(fn, cols, w, nullptr, w_dt)) != MXQ_OK) return st;
+  if ((st = check_plane(fn, "x", x, rows, cols, ld_x, codes ? 1 : dtype_bytes(dt), 16)) != MXQ_OK) return st;
+  if ((st = check_plane(fn, "dx", dx, rows, cols, ld_dx, dtype_bytes(dt), 16)) != MXQ_OK) return st;
+  if ((st = check_row_values(fn, "x_scales", x_scales, rows, true)) != MXQ_OK) return st;
+  if ((st = check_row_values(fn, "mean", mean, rows, false)) != MXQ_OK) return st;
+  if ((st = check_row_values(fn, "rstd", rstd, rows, false)) != MXQ_OK) return st;
+  if (!dw != !db) return fail(MXQ_ERR_INVALID_ARG, "%s: dw and db must be given together", fn);
+  if (!aligned(dw, 16) || !aligned(db, 16)) return fail(MXQ_ERR_INVALID_ARG, "%s: dw and db must be 16-byte aligned", fn);
+  const size_t need = dw ? mxq_layer_norm_backward_workspace_bytes(rows, cols) : 0;
+  if (need > 0 && (!workspace || !aligned(workspace, 16) || ws_bytes < need))
+    return fail(MXQ_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned and hold %llu bytes", fn, (unsigned long long)need);
+  mxq::NormGradParams p;
+  p.dy = dy;
+  p.x = x;
+  p.x_scales = x_scales;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.w = w;
+  p.dx = dx;
+  p.dw = dw;
+  p.db = db;
+  p.part = static_cast<float*>(workspace);
+  p.rows = rows;
+  p.ld_dy = ld_dy;
+  p.ld_x = ld_x;
+  p.ld_dx = ld_dx;
+  p.units = (uint32_t)(cols / 8);
+  p.w_f32 = w_dt == MXQ_F32 ? 1 : 0;
+  p.inv_cols = 1.0f / (float)cols;
+  return hip_status(fn, mxq::launch_layer_norm_backward(p, dt == MXQ_F32, codes, as_stream(stream)));
+}
+
+mxq_status mxq_activation(const void* u, mxq_dtype dt, int64_t rows, int64_t cols, int64_t ld_u, mxq_activation_kind act,
+                          void* y, int64_t ld_y, int8_t* u_codes, int64_t ld_uc, float* u_scales, void* stream) {
+  return activation("mxq_activation", u, dt, rows, cols, ld_u, act, y, ld_y, nullptr, u_codes, ld_uc, u_scales, false,
+                    as_stream(stream));
+}
+
+mxq_status mxq_quantize_activation(const void* u, mxq_dtype dt, int64_t rows, int64_t cols, int64_t ld_u,
+                                   mxq_activation_kind act, int8_t* codes, int64_t ld_codes, float* scales,
+                                   int8_t* u_codes, int64_t ld_uc, float* u_scales, void* stream) {
+  return activation("mxq_quantize_activation", u, dt, rows, cols, ld_u, act, codes, ld_codes, scales, u_codes, ld_uc,
+                    u_scales, true, as_stream(stream));
+}
+
+mxq_status mxq_activation_backward(const void* dy, mxq_dtype dt, int64_t rows, int64_t cols, int64_t ld_dy,
+                                   const int8_t* u_codes, int64_t ld_uc, const float* u_scales, mxq_activation_kind act,
+                                   void* du, int64_t ld_du, void* stream) {
+  const char* fn = "mxq_activation_backward";
+  mxq_status st = check_act(fn, act);
+  if (st != MXQ_OK) return st;
+  if ((st = check_input(fn, dy, dt, rows, cols, ld_dy, 16)) != MXQ_OK) return st;
+  if ((st = check_plane(fn, "u_codes", u_codes, rows, cols, ld_uc, 1, 16)) != MXQ_OK) return st;
+  if ((st = check_plane(fn, "du", du, rows, cols, ld_du, dtype_bytes(dt), 16)) != MXQ_OK) return st;
+  if ((st = check_row_values(fn, "u_scales", u_scales, rows, false)) != MXQ_OK) return st;
+  mxq::ActGradParams p;
+  p.dy = dy;
+  p.kept = u_codes;
+  p.kept_scales = u_scales;
+  p.dx = du;
+  p.ld_dy = ld_dy;
+  p.ld_kept = ld_uc;
+  p.ld_dx = ld_du;
+  p.units = (uint32_t)(cols / 8);
+  p.total = (uint32_t)(rows * (cols / 8));
+  return hip_status(fn, mxq::launch_activation_backward(
+                            p, dt == MXQ_F32, act == MXQ_ACT_GELU_TANH ? mxq::ACT_GELU_TANH : mxq::ACT_SILU, as_stream(stream)));
+}
+
+size_t mxq_grad_weight_int8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return grad_shape_ok(M, N, K) ? mxq::grad_weight_workspace_bytes(M, N, K) : 0;
+}
+
+mxq_status mxq_grad_weight_int8(const uint16_t* dy, int64_t ld_dy, const int8_t* codes, int64_t ld_codes,
+                                const float* scales, int64_t M, int64_t N, int64_t K, void* out, mxq_dtype out_dt,
+                                int64_t ld_out, int accumulate, void* workspace, size_t ws_bytes, void* stream) {
+  const char* fn = "mxq_grad_weight_int8";
+  const int ob = dtype_bytes(out_dt);
+  if (ob == 0) return fail(MXQ_ERR_UNSUPPORTED, "%s: unknown output dtype %d", fn, (int)out_dt);
+  if (M < 0 || N < 0 || K < 0)
+    return fail(MXQ_ERR_INVALID_ARG, "%s: negative size (M=%lld N=%lld K=%lld)", fn, (long long)M, (long long)N, (long long)K);
+  if (N % 8 != 0) return fail(MXQ_ERR_INVALID_ARG, "%s: N (%lld) must be a multiple of 8", fn, (long long)N);
+  if (K % 16 != 0) return fail(MXQ_ERR_INVALID_ARG, "%s: K (%lld) must be a multiple of 16", fn, (long long)K);
+  if (N > 0 && K > 0 && !grad_shape_ok(M, N, K)) return fail(MXQ_ERR_INVALID_ARG, "%s: problem too large", fn);
+  if (ld_dy >= ((int64_t)1 << 23)) return fail(MXQ_ERR_INVALID_ARG, "%s: ld of dy (%lld) must be below 2^23", fn, (long long)ld_dy);
+  mxq_status st = check_plane(fn, "dy", dy, K > 0 ? M : 0, N, ld_dy, 2, 16);
+  if (st != MXQ_OK) return st;
+  if ((st = check_plane(fn, "codes", codes, N > 0 ? M : 0, K, ld_codes, 1, 16)) != MXQ_OK) return st;
+  if ((st = check_plane(fn, "out", out, N, K, ld_out, ob, ob)) != MXQ_OK) return st;
+  if (N == 0 || K == 0) return ok();
+  if ((st = check_row_values(fn, "scales", scales, M, false)) != MXQ_OK) return st;
+  const size_t need = mxq_grad_weight_int8_workspace_bytes(M, N, K);
+  if (need > 0 && (!workspace || !aligned(workspace, 16) || ws_bytes < need))
+    return fail(MXQ_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned and hold %llu bytes", fn, (unsigned long long)need);
+  return hip_status(fn, mxq::launch_grad_weight_int8(dy, ld_dy, codes, ld_codes, scales, M, N, K, out, out_dt == MXQ_F32,
+                                                     ld_out, accumulate != 0, workspace, as_stream(stream)));
 }
 
 }  // extern "C"

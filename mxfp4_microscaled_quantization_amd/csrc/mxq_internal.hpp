@@ -83,6 +83,69 @@ struct QkNormParams {
 };
 hipError_t launch_qk_norm_rope(const QkNormParams& p, bool f32, bool quant, bool halves, hipStream_t stream);
 
+// Layer norm and its gradient (layer_norm.hip).  units: columns / 8; pitches in elements of
+// the tensor they belong to.
+struct NormParams {
+  const void* x;
+  const void *w, *b;       // weights and biases of one type, either may be null
+  void* y;                 // the input's type, or int8 codes
+  float* scales;           // of the codes
+  float *mean, *rstd;      // or both null
+  int8_t* kept;            // codes of x, or null
+  float* kept_scales;
+  int64_t rows, ld_x, ld_y, ld_kept;
+  uint32_t units;
+  int w_f32;
+  float eps, inv_cols;
+};
+hipError_t launch_layer_norm(const NormParams& p, bool f32, bool quant, hipStream_t stream);
+
+constexpr int kNormThreads = 1024;   // of the gradient's largest workgroup, with up to 2 units each
+constexpr int64_t kNormMaxCols = 8 * 2 * kNormThreads;
+struct NormGradParams {
+  const void *dy, *x;      // x: of dy's type, or int8 codes
+  const float *x_scales, *mean, *rstd;
+  const void* w;           // or null
+  void* dx;
+  float *dw, *db;          // both null: no weights
+  float* part;             // sums of the workgroups
+  int64_t rows, ld_dy, ld_x, ld_dx;
+  uint32_t units;
+  int w_f32;
+  float inv_cols;
+};
+size_t layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+hipError_t launch_layer_norm_backward(const NormGradParams& p, bool f32, bool codes, hipStream_t stream);
+
+// The feed-forward activation, its 8-bit checkpoint and its gradient (activation.hip).
+enum ActKind { ACT_GELU_TANH = 0, ACT_SILU = 1 };
+constexpr int64_t kActMaxCols = 8 * 8 * 1024;   // of the forward pass
+struct ActParams {
+  const void* u;
+  void* y;                 // the input's type, or int8 codes
+  float* scales;           // of the codes
+  int8_t* kept;            // checkpoint, or null
+  float* kept_scales;
+  int64_t rows, ld_u, ld_y, ld_kept;
+  uint32_t units;
+};
+hipError_t launch_activation(const ActParams& p, bool f32, bool quant, ActKind act, hipStream_t stream);
+struct ActGradParams {
+  const void* dy;
+  const int8_t* kept;
+  const float* kept_scales;
+  void* dx;
+  int64_t ld_dy, ld_kept, ld_dx;
+  uint32_t units, total;   // of a row, of all rows
+};
+hipError_t launch_activation_backward(const ActGradParams& p, bool f32, ActKind act, hipStream_t stream);
+
+// Weight gradient of the 8-bit product (grad_weight.hip): out (+)= dy^T * bf16(code * scale).
+size_t grad_weight_workspace_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_grad_weight_int8(const uint16_t* dy, int64_t ld_dy, const int8_t* codes, int64_t ld_codes,
+                                   const float* scales, int64_t M, int64_t N, int64_t K, void* out, bool f32_out,
+                                   int64_t ld_out, bool accumulate, void* workspace, hipStream_t stream);
+
 size_t sqnr_workspace_bytes(int64_t n);
 // The library's own SQNR workspace on the current device (a static device array,
 // sqnr_scratch_bytes() long): its device address, looked up once per device.

@@ -1,0 +1,87 @@
+// Helpers of the kernels that take a row of a matrix as units of 8 elements (layer_norm.hip,
+// activation.hip): a unit as 8 binary32 values and back, and sums over the lanes of a wave.
+#pragma once
+
+#include <type_traits>
+
+#include "mxq_int8.hpp"
+
+namespace mxq {
+
+template <bool F32>
+__device__ __forceinline__ void widen_unit(const Unit<F32>& u, float (&v)[8]) {
+  if constexpr (F32) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = __int_as_float(u.d[0][e]);
+      v[4 + e] = __int_as_float(u.d[1][e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] = bf16_lo_f32(u.d[0][e]);
+      v[2 * e + 1] = bf16_hi_f32(u.d[0][e]);
+    }
+  }
+}
+
+// Rounds once, to nearest even, where the output is bf16.  PAST: stored past the caches.
+template <bool F32, bool PAST>
+__device__ __forceinline__ void store_unit(void* y, int64_t elem, const float (&v)[8]) {
+  auto put = [](v4i* p, v4i d) {
+    if constexpr (PAST)
+      __builtin_nontemporal_store(d, p);
+    else
+      *p = d;
+  };
+  if constexpr (F32) {
+    v4i* p = reinterpret_cast<v4i*>(static_cast<float*>(y) + elem);
+    put(p, v4i{__float_as_int(v[0]), __float_as_int(v[1]), __float_as_int(v[2]), __float_as_int(v[3])});
+    put(p + 1, v4i{__float_as_int(v[4]), __float_as_int(v[5]), __float_as_int(v[6]), __float_as_int(v[7])});
+  } else {
+    put(reinterpret_cast<v4i*>(static_cast<uint16_t*>(y) + elem),
+        v4i{(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3]), (int)pack_bf16x2(v[4], v[5]),
+            (int)pack_bf16x2(v[6], v[7])});
+  }
+}
+
+// The 8 codes of a unit as values fl32(code * scale): the product is rounded by itself, also where a sum follows.
+__device__ __forceinline__ void widen_codes(v2u c, float s, float (&v)[8]) {
+#pragma clang fp contract(off)
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[4 * h + e] = (float)(int8_t)(c[h] >> (8 * e)) * s;
+}
+
+__device__ __forceinline__ v2u pack_codes(const float (&v)[8], const Int8Scale& sc) {
+  return v2u{int8_pack4(v[0], v[1], v[2], v[3], sc.inv) & sc.keep, int8_pack4(v[4], v[5], v[6], v[7], sc.inv) & sc.keep};
+}
+
+// Largest |v| as a binary32 pattern: a NaN wins over an infinity, which wins over finite values.
+__device__ __forceinline__ unsigned max_abs8(const float (&v)[8]) {
+  unsigned m = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+  return m;
+}
+
+// Sum over each 16 lanes, or the 64 of a wave, the same bits in every lane.
+__device__ __forceinline__ float row16_sum(float v) {
+  auto dpp = [](float x, auto ctrl) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), decltype(ctrl)::value, 0xF, 0xF, false));
+  };
+  v += dpp(v, std::integral_constant<int, 0xB1>{});    // lane ^ 1
+  v += dpp(v, std::integral_constant<int, 0x4E>{});    // lane ^ 2
+  v += dpp(v, std::integral_constant<int, 0x141>{});   // row_half_mirror: the other quad of 8
+  v += dpp(v, std::integral_constant<int, 0x140>{});   // row_mirror: the other 8 of 16
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = row16_sum(v);
+  v += __shfl_xor(v, 16);
+  v += __shfl_xor(v, 32);
+  return v;
+}
+
+}  // namespace mxq

@@ -23,6 +23,8 @@ exact integer / rational arithmetic) unless the method fixes a precision:
 * ``int8``     -- 8-bit row quantization and the 8-bit product with token and channel
   scales.
 * ``qk_norm``  -- root-mean-square norm of query and key heads with the position rotation.
+* ``training`` -- layer norm and its gradient, the feed-forward activation with its 8-bit
+  checkpoint, and the weight gradient of the 8-bit product.
 
 Sources (web pages, cited by title and section):
 * "AMD Quark adds native W4A8 mixed-precision for Wan2.2 video generation on MI350",
@@ -46,7 +48,7 @@ Parity status: every public function is pinned by the ``-m "not gpu"`` tests aga
 closed forms, library routines, exact rational brute force or invariants.
 """
 
-from . import formats, mxfp4, fp8, gemm, sqnr, hadamard, int8, qk_norm  # noqa: F401
+from . import formats, mxfp4, fp8, gemm, sqnr, hadamard, int8, qk_norm, training  # noqa: F401
 from .formats import (  # noqa: F401
     E2M1_MAGNITUDES, e2m1_decode, e8m0_decode, e4m3_decode, E4M3_MAX,
     bf16_bits_to_f64, f64_to_bf16_bits, bf16_ulp,
