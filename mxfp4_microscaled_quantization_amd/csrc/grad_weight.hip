@@ -23,14 +23,14 @@ struct GradParams {
   const uint16_t* dy;
   const uint16_t* x;
   void* out;
-  float* part;              // sums of the parts of M, [splits][N][K]
+  float* part;              // sums of the parts of M, [tile - whole][splits][rows of a tile][columns]
   int64_t ld_dy, ld_x, ld_out;
   int M, N, K;
-  int nwin, tiles_n, tiles_k, splits;
+  int nwin, tiles_n, tiles_k;
+  int whole, splits;        // tiles whose workgroup takes all of M; parts of M for each of the others
   int accumulate, vec;      // vec: rows of the output are aligned for whole stores of 4
 };
 
-enum { GRAD_BF16 = 0, GRAD_F32 = 1, GRAD_PART = 2 };
 
 // MI x MJ fragments of 16 x 16 outputs (k, n) in a wave, WK x WN waves.
 template <int MI, int MJ, int WK, int WN>
@@ -43,18 +43,32 @@ __device__ __forceinline__ void grad_line_to_lds(__amdgpu_buffer_rsrc_t r, uint8
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds_line, 16, voff, soff, 0, 0);
 }
 
+// __restrict__ tells the compiler that no load into LDS in flight is what this reads: without it, it waits for all of
+// them before the read (the hand-overs wait for what has to have landed).
 typedef short v4s __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ v2u read_transposed(const uint8_t* lds) {
-  return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)lds));
+__device__ __forceinline__ v2u read_transposed(__attribute__((address_space(3))) v4s* __restrict__ lds) {
+  return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds));
 }
 
-// 4 sums of columns k .. k + 3 of row n (some of them past K unless `whole`).
-template <int OUT>
+// Tile `seq`: bands of kGradBand tiles along K, in which the index runs along K first, so that the tiles an XCD runs at once
+// share their panels in its L2.
+constexpr int kGradBand = 4;
+__device__ __forceinline__ void grad_tile_at(const GradParams& p, int seq, int& tk, int& tn) {
+  const int band = seq / (kGradBand * p.tiles_n), first = band * kGradBand, rows = min(kGradBand, p.tiles_k - first);
+  const int in = seq - band * kGradBand * p.tiles_n;
+  tk = first + in % rows;
+  tn = in / rows;
+}
+// Workgroups are dealt to the XCDs in turn: a contiguous run of n indexes for each.
+__device__ __forceinline__ int grad_xcd_run(int bid, int n) {
+  const int xcd = bid & 7, q8 = n >> 3, r8 = n & 7;
+  return xcd * q8 + min(xcd, r8) + (bid >> 3);
+}
+
+// 4 sums of columns k .. k + 3 of row n; K is a multiple of 16, so that all are there.
+template <bool F32OUT>
 __device__ __forceinline__ void store_sums(const GradParams& p, int n, int k, v4f v) {
-  if constexpr (OUT == GRAD_PART) {
-    // K is a multiple of 16, and so is every part's row
-    *reinterpret_cast<v4f*>(p.part + ((int64_t)blockIdx.y * p.N + n) * p.K + k) = v;
-  } else if constexpr (OUT == GRAD_F32) {
+  if constexpr (F32OUT) {
     float* o = static_cast<float*>(p.out) + (int64_t)n * p.ld_out + k;
     if (p.vec) {
       if (p.accumulate) v += *reinterpret_cast<const v4f*>(o);
@@ -80,45 +94,104 @@ __device__ __forceinline__ void store_sums(const GradParams& p, int n, int k, v4
   }
 }
 
-template <int OUT, int MI, int MJ, int WK, int WN>
+// s_waitcnt immediate (gfx9 encoding): vmcnt <= vm, lgkmcnt <= 0, expcnt unconstrained
+constexpr int grad_wait_vm(int vm) { return (vm & 0xF) | ((vm >> 4) << 14) | (0x7 << 4); }
+
+// which of n loads spread over rd reads go out right after read k
+constexpr int grad_loads_after(int k, int n, int rd) { return (k + 1) * n / rd - k * n / rd; }
+
+// Scheduling pattern of one MFMA region: unit I is the two reads of a fragment, then the tile loads
+// that fall there, then its share of the region's MFMAs.
+template <int ID, int R, int MFMAS, int VM, int I>
+__device__ __forceinline__ void grad_region_unit() {
+  __builtin_amdgcn_sched_group_barrier(0x100, 2, ID);                                    // DS read
+  constexpr int l = grad_loads_after(I, VM, R);
+  if constexpr (l > 0) __builtin_amdgcn_sched_group_barrier(0x020, l, ID);               // VMEM read
+  constexpr int n = (I + 1) * MFMAS / R - I * MFMAS / R;
+  if constexpr (n > 0) __builtin_amdgcn_sched_group_barrier(0x008, n, ID);               // MFMA
+}
+template <int ID, int R, int MFMAS, int VM, int... Is>
+__device__ __forceinline__ void grad_region(std::integer_sequence<int, Is...>) {
+  (grad_region_unit<ID, R, MFMAS, VM, Is>(), ...);
+}
+
+template <bool F32OUT, int MI, int MJ, int WK, int WN>
 __global__ __launch_bounds__(64 * WK * WN, 1) void grad_weight_kernel(GradParams p) {
   using T = GradTile<MI, MJ, WK, WN>;
-  constexpr int WAVES = WK * WN;
+  constexpr int WAVES = WK * WN, NX = 2, NY = 3;   // ring depths
   constexpr int LX = (int)(T::X_TILE / 1024) / WAVES, LY = (int)(T::Y_TILE / 1024) / WAVES;   // 1 KB lines per wave
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::X_TILE + T::Y_TILE];
-  uint8_t* const lx = lds;
-  uint8_t* const ly = lds + T::X_TILE;
+  constexpr int RD = MI + MJ, VM = LX + LY;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NX * T::X_TILE + NY * T::Y_TILE];
+  constexpr uint32_t Y_BASE = NX * T::X_TILE;
 
   const uint32_t tid = threadIdx.x, lane = tid & 63;
   const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(tid >> 6));
   const uint32_t wk = wave % WK, wn = wave / WK;
-  const int tile = blockIdx.x, k0 = tile / p.tiles_n * T::BK, n0 = tile % p.tiles_n * T::BN;
-  const int w_lo = OUT == GRAD_PART ? (int)((int64_t)blockIdx.y * p.nwin / p.splits) : 0;
-  const int w_hi = OUT == GRAD_PART ? (int)((int64_t)(blockIdx.y + 1) * p.nwin / p.splits) : p.nwin;
+  // this workgroup's tile, and its windows of M: all, or one of the parts (part by part, so that
+  // what runs at once shares its rows)
+  int seq, part = -1, w_lo = 0, w_hi = p.nwin;
+  if ((int)blockIdx.x < p.whole) {
+    seq = grad_xcd_run(blockIdx.x, p.whole);
+  } else {
+    const int rest = p.tiles_n * p.tiles_k - p.whole, i = grad_xcd_run((int)blockIdx.x - p.whole, rest * p.splits);
+    part = i / rest;
+    seq = p.whole + i - part * rest;
+    w_lo = (int)((int64_t)part * p.nwin / p.splits);
+    w_hi = (int)((int64_t)(part + 1) * p.nwin / p.splits);
+  }
+  int tk, tn;
+  grad_tile_at(p, seq, tk, tn);
+  // quotients are formed in vector registers: back to scalar ones, for the resources
+  auto scalar = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+  const int k0 = scalar(tk) * T::BK, n0 = scalar(tn) * T::BN;
+  w_lo = scalar(w_lo);
+  w_hi = scalar(w_hi);
 
-  // A window's rows start at r0: a resource of its own for each (64-bit base, offsets below 2^31)
-  auto rows_of = [&](const uint16_t* base, int64_t ld, int cols, int col0, int w) {
-    const int left = p.M - w * kWinRows, rows = left < kWinRows ? left : kWinRows;
-    const uint32_t bytes = rows > 0 ? (uint32_t)(((int64_t)(rows - 1) * ld + cols - col0) * 2) : 0u;
-    return make_rsrc(base + (int64_t)w * kWinRows * ld + col0, bytes);
+  // A window's rows have a resource of their own (64-bit base, offsets below 2^31), empty past the part's
+  // last window, so that the loads in flight stay what the waits assume.  An empty one's size comes out as the
+  // unused end of a row, negated.
+  const int m_hi = min(p.M, w_hi * kWinRows);
+  auto rows_of = [&](const uint16_t* base, int ld, int cols, int col0, int w) {
+    const int rows = max(0, min(m_hi - w * kWinRows, kWinRows));
+    const int elems = scalar(max(rows * ld - (ld - (cols - col0)), 0));
+    return make_rsrc(base + (int64_t)w * kWinRows * ld + col0, (uint32_t)elems * 2u);
   };
   // LDS: rows of BC columns, 32-byte unit u of row r at u ^ (r & 7) (the 8 rows that half a wave
-  // reads at one column are then on distinct banks)
-  auto fill = [&](__amdgpu_buffer_rsrc_t r, uint8_t* to, uint32_t ld, auto bc_tag, auto lines_tag) {
+  // reads at one column are then on distinct banks).  Line `line` of a window, by one wave:
+  auto fill = [&](__amdgpu_buffer_rsrc_t r, uint8_t* to, uint32_t ld, uint32_t line, auto bc_tag) {
     constexpr uint32_t BC = decltype(bc_tag)::value, CPR = BC / 8, RPL = 64 / CPR;   // 16-byte chunks per row, rows per line
-    constexpr int L = decltype(lines_tag)::value;
-#pragma unroll
-    for (int j = 0; j < L; ++j) {
-      const uint32_t line = wave * L + j, row = line * RPL + lane / CPR, slot = lane % CPR;
-      grad_line_to_lds(r, to + line * 1024, row * ld * 2 + ((slot ^ ((row & 7) << 1)) << 4), 0);
-    }
+    const uint32_t row = line * RPL + lane / CPR, slot = lane % CPR;
+    grad_line_to_lds(r, to + line * 1024, lane / CPR * ld * 2 + ((slot ^ ((row & 7) << 1)) << 4), line * RPL * ld * 2);
   };
-  // the fragment of 16 columns from c0, tokens 32 t + 4 g + (0 .. 3) and 16 more, g = lane / 16
-  auto read = [&](const uint8_t* from, uint32_t pitch, uint32_t c0, int t) {
-    const uint32_t q = lane & 15, row = 32 * t + 4 * (lane >> 4) + (q >> 2);
-    const uint32_t unit = c0 / 16, at = row * pitch + ((unit ^ (row & 7)) << 5) + 8 * (q & 3);
-    const v2u lo = read_transposed(from + at), hi = read_transposed(from + at + 16 * pitch);
+  const int ld_x = (int)p.ld_x, ld_dy = (int)p.ld_dy;
+  auto x_rows = [&](int w) { return rows_of(p.x, ld_x, p.K, k0, w); };
+  auto y_rows = [&](int w) { return rows_of(p.dy, ld_dy, p.N, n0, w); };
+  auto issue_x = [&](__amdgpu_buffer_rsrc_t r, uint32_t slot, int j) {
+    fill(r, lds + slot * T::X_TILE, (uint32_t)p.ld_x, wave * LX + j, std::integral_constant<uint32_t, T::BK>{});
+  };
+  auto issue_y = [&](__amdgpu_buffer_rsrc_t r, uint32_t slot, int j) {
+    fill(r, lds + Y_BASE + slot * T::Y_TILE, (uint32_t)p.ld_dy, wave * LY + j, std::integral_constant<uint32_t, T::BN>{});
+  };
+  // the fragment of 16 columns from unit u, tokens 32 t + 4 g + (0 .. 3) and 16 more, g = lane / 16
+  const uint32_t q = lane & 15, row0 = 4 * (lane >> 4) + (q >> 2);
+  const uint32_t at_x = row0 * (T::BK * 2) + ((row0 & 7) << 5) + 8 * (q & 3), at_y = row0 * (T::BN * 2) + ((row0 & 7) << 5) + 8 * (q & 3);
+  auto read1 = [&](const uint8_t* tile_at, uint32_t pitch, uint32_t at, uint32_t u, int t) {
+    const uint8_t* from = tile_at + (at ^ (u << 5)) + 32 * t * pitch;
+    const v2u lo = read_transposed((__attribute__((address_space(3))) v4s*)from);
+    const v2u hi = read_transposed((__attribute__((address_space(3))) v4s*)(from + 16 * pitch));
     return v4u{lo[0], lo[1], hi[0], hi[1]};
+  };
+  auto read = [&](v4u(&f)[RD], uint32_t sx, uint32_t sy, int t, auto&& after) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      f[i] = read1(lds + sx * T::X_TILE, T::BK * 2, at_x, wk * MI + i, t);
+      after(i);
+    }
+#pragma unroll
+    for (int j = 0; j < MJ; ++j) {
+      f[MI + j] = read1(lds + Y_BASE + sy * T::Y_TILE, T::BN * 2, at_y, wn * MJ + j, t);
+      after(MI + j);
+    }
   };
 
   v4f acc[MI][MJ];
@@ -126,68 +199,132 @@ __global__ __launch_bounds__(64 * WK * WN, 1) void grad_weight_kernel(GradParams
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < MJ; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  auto step = [&](const v4u(&f)[RD]) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int jj = 0; jj < MJ; ++jj) {
+        const int j = i & 1 ? MJ - 1 - jj : jj;
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f[i]),
+                                                            __builtin_bit_cast(bf16x8, f[MI + j]), acc[i][j], 0, 0, 0);
+      }
+  };
+  auto barrier = [] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
 
-  for (int w = w_lo; w < w_hi; ++w) {
+  // prologue: window w_lo resident; then, in the order the steady state issues them, x of the next window, and dy of
+  // the next two (y of w+1 first: the hand-over leaves only the last in flight)
+  v4u f0[RD], f1[RD];
+  if (w_lo < w_hi) {
+#pragma unroll
+    for (int j = 0; j < LX; ++j) issue_x(x_rows(w_lo), 0, j);
+#pragma unroll
+    for (int j = 0; j < LY; ++j) issue_y(y_rows(w_lo), 0, j);
+    __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
-    fill(rows_of(p.x, p.ld_x, p.K, k0, w), lx, (uint32_t)p.ld_x, std::integral_constant<uint32_t, T::BK>{}, std::integral_constant<int, LX>{});
-    fill(rows_of(p.dy, p.ld_dy, p.N, n0, w), ly, (uint32_t)p.ld_dy, std::integral_constant<uint32_t, T::BN>{}, std::integral_constant<int, LY>{});
-    __syncthreads();
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      v4u fx[MI], fy[MJ];
+    for (int j = 0; j < LY; ++j) issue_y(y_rows(w_lo + 1), 1, j);
 #pragma unroll
-      for (int i = 0; i < MI; ++i) fx[i] = read(lx, T::BK * 2, (wk * MI + i) * 16, t);
+    for (int j = 0; j < LX; ++j) issue_x(x_rows(w_lo + 1), 1, j);
 #pragma unroll
-      for (int j = 0; j < MJ; ++j) fy[j] = read(ly, T::BN * 2, (wn * MJ + j) * 16, t);
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < MJ; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fx[i]),
-                                                              __builtin_bit_cast(bf16x8, fy[j]), acc[i][j], 0, 0, 0);
-    }
+    for (int j = 0; j < LY; ++j) issue_y(y_rows(w_lo + 2), 2, j);
+    read(f0, 0, 0, 0, [](int) {});
   }
-  // lane l holds columns k 4 (l / 16) .. + 3 of row n l % 16 of each block; K is a multiple of 16
+  // One window: step 0 on f0 under the reads of step 1 into f1; the hand-over waits for window w+1 (only dy of window
+  // w+2 may still be in flight) and releases window w's slots; step 1 on f1 under the reads of window w+1's step 0 and the
+  // loads of x of window w+2 and dy of window w+3 into those slots.
+  uint32_t sx = 0, sy = 0;
+  for (int w = w_lo; w < w_hi; ++w) {
+    const __amdgpu_buffer_rsrc_t rx = x_rows(w + NX), ry = y_rows(w + NY);
+    const uint32_t sx1 = sx ^ 1, sy1 = sy == NY - 1 ? 0 : sy + 1;
+    read(f1, sx, sy, 1, [](int) {});
+    step(f0);
+    grad_region<0, RD, MI * MJ, 0>(std::make_integer_sequence<int, RD>{});
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(grad_wait_vm(LY));
+    barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    read(f0, sx1, sy1, 0, [&](int k) {
+      if (grad_loads_after(k, VM, RD) > 0) {
+        const int j = k * VM / RD;
+        if (j < LX)
+          issue_x(rx, sx, j);
+        else
+          issue_y(ry, sy, j - LX);
+      }
+    });
+    step(f1);
+    grad_region<1, RD, MI * MJ, VM>(std::make_integer_sequence<int, RD>{});
+    __builtin_amdgcn_sched_barrier(0);
+    sx = sx1;
+    sy = sy1;
+  }
+  // lane l holds columns k 4 (l / 16) .. + 3 of row n l % 16 of each block
+  float* const sums = part >= 0 ? p.part + ((int64_t)(seq - p.whole) * p.splits + part) * (T::BN * T::BK) : nullptr;
 #pragma unroll
   for (int j = 0; j < MJ; ++j) {
-    const int n = n0 + (int)(wn * MJ + j) * 16 + (int)(lane & 15);
-    if (n < p.N) {
+    const int nl = (int)(wn * MJ + j) * 16 + (int)(lane & 15);
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const int k = k0 + (int)(wk * MI + i) * 16 + 4 * (int)(lane >> 4);
-        if (k < p.K) store_sums<OUT>(p, n, k, acc[i][j]);
+    for (int i = 0; i < MI; ++i) {
+      const int kl = (int)(wk * MI + i) * 16 + 4 * (int)(lane >> 4);
+      if (n0 + nl < p.N && k0 + kl < p.K) {
+        if (sums)
+          *reinterpret_cast<v4f*>(sums + nl * T::BK + kl) = acc[i][j];
+        else
+          store_sums<F32OUT>(p, n0 + nl, k0 + kl, acc[i][j]);
       }
     }
   }
+  __builtin_amdgcn_s_waitcnt(grad_wait_vm(0));   // no load into LDS outlives the workgroup
 }
 
-// Joins the parts of M in order; 4 columns for each thread.
-template <int OUT>
+// Joins the parts of M of the tiles from p.whole on, in order; 4 columns for each thread, blockIdx.y the tile.
+template <bool F32OUT, int BN, int BK>
 __global__ __launch_bounds__(256) void grad_weight_sums_kernel(GradParams p) {
-  const int64_t quads = (int64_t)p.N * (p.K / 4);
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= quads) return;
-  v4f v = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s = 0; s < p.splits; ++s) v += *reinterpret_cast<const v4f*>(p.part + ((int64_t)s * quads + i) * 4);
-  const int n = (int)(i / (p.K / 4)), k = (int)(i - (int64_t)n * (p.K / 4)) * 4;
-  store_sums<OUT>(p, n, k, v);
+  int tk, tn;
+  grad_tile_at(p, p.whole + (int)blockIdx.y, tk, tn);
+  const int i = (int)blockIdx.x * 256 + (int)threadIdx.x, nl = i / (BK / 4), kl = i % (BK / 4) * 4;
+  const int n = tn * BN + nl, k = tk * BK + kl;
+  if (n >= p.N || k >= p.K) return;
+  const float* from = p.part + (int64_t)blockIdx.y * p.splits * (BN * BK) + nl * BK + kl;
+  v4f v = *reinterpret_cast<const v4f*>(from);
+#pragma unroll 4
+  for (int s = 1; s < p.splits; ++s) v += *reinterpret_cast<const v4f*>(from + (int64_t)s * (BN * BK));
+  store_sums<F32OUT>(p, n, k, v);
 }
 
+// Which tile, and how the tiles share the GPU: as many whole rounds of it as there are, and the rest of the
+// tiles cut into parts of M.  Times in us.
 struct GradPlan {
-  int big, splits, tiles_n, tiles_k;
+  int size, splits, tiles_n, tiles_k, whole;
 };
 GradPlan plan_grad(int64_t M, int64_t N, int64_t K) {
-  GradPlan g;
-  const int64_t t256 = ((N + 255) / 256) * ((K + 255) / 256);
-  g.big = t256 >= 128;
-  const int64_t b = g.big ? 256 : 128, nwin = (M + kWinRows - 1) / kWinRows;
-  g.tiles_n = (int)((N + b - 1) / b);
-  g.tiles_k = (int)((K + b - 1) / b);
-  const int64_t tiles = (int64_t)g.tiles_n * g.tiles_k;
-  int64_t s = 1;
-  while (!g.big && tiles * s * 2 <= 512 && nwin / (s * 2) >= 4) s *= 2;
-  g.splits = (int)s;
-  return g;
+  GradPlan best = {};
+  double least = 0.0;
+  const int nwin = (int)((M + kWinRows - 1) / kWinRows);
+  for (const int size : {256, 128}) {
+    const int64_t slots = size == 256 ? 256 : 512;                  // workgroups at once
+    const double window = size == 256 ? 1.9 : 1.25, ends = 6.0;     // of a workgroup on a full GPU
+    const int64_t tn = (N + size - 1) / size, tk = (K + size - 1) / size, tiles = tn * tk;
+    const int64_t whole = tiles / slots * slots, rest = tiles - whole;
+    const double base = (double)(whole / slots) * (nwin * window + ends);
+    for (int s = 1; s == 1 || (s * 2 <= nwin && rest * s <= 4 * slots); ++s) {
+      double t = base;
+      if (rest > 0) {
+        t += (double)((rest * s + slots - 1) / slots) * ((nwin + s - 1) / s * window + ends);
+        if (s > 1) t += 5.0 + (double)(rest * s * size * size) * 8.0 / 4e6;
+      }
+      if (least == 0.0 || t < least) {
+        least = t;
+        best = {size, s, (int)tn, (int)tk, s > 1 ? (int)whole : (int)tiles};
+      }
+      if (rest == 0) break;
+    }
+  }
+  return best;
 }
 
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
@@ -196,7 +333,7 @@ size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
 size_t grad_weight_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   const GradPlan g = plan_grad(M, N, K);
-  return round256((size_t)M * (size_t)K * 2) + (g.splits > 1 ? (size_t)g.splits * (size_t)N * (size_t)K * 4 : 0);
+  return round256((size_t)M * (size_t)K * 2) + (size_t)(g.tiles_n * g.tiles_k - g.whole) * g.splits * g.size * g.size * 4;
 }
 
 hipError_t launch_grad_weight_int8(const uint16_t* dy, int64_t ld_dy, const int8_t* codes, int64_t ld_codes,
@@ -221,31 +358,28 @@ hipError_t launch_grad_weight_int8(const uint16_t* dy, int64_t ld_dy, const int8
   p.nwin = (int)((M + kWinRows - 1) / kWinRows);
   p.tiles_n = g.tiles_n;
   p.tiles_k = g.tiles_k;
+  p.whole = g.whole;
   p.splits = g.splits;
   p.accumulate = accumulate;
   const uintptr_t step = f32_out ? 4 : 2;
   p.vec = reinterpret_cast<uintptr_t>(out) % (4 * step) == 0 && ld_out % 4 == 0;
-  auto go = [&](auto out_tag) {
-    constexpr int OUT = decltype(out_tag)::value;
-    const dim3 grid((unsigned)(g.tiles_n * g.tiles_k), (unsigned)g.splits);
-    if (g.big)
-      hipLaunchKernelGGL((grad_weight_kernel<OUT, 4, 8, 4, 2>), grid, dim3(512), 0, stream, p);
-    else
-      hipLaunchKernelGGL((grad_weight_kernel<OUT, 2, 4, 4, 2>), grid, dim3(512), 0, stream, p);
+  const int rest = g.tiles_n * g.tiles_k - g.whole;
+  const unsigned grid = (unsigned)(g.whole + rest * g.splits);
+  auto go = [&](auto f_tag, auto mi_tag, auto mj_tag) {
+    constexpr bool F = decltype(f_tag)::value;
+    constexpr int MI = decltype(mi_tag)::value, MJ = decltype(mj_tag)::value;
+    using T = GradTile<MI, MJ, 4, 2>;
+    hipLaunchKernelGGL((grad_weight_kernel<F, MI, MJ, 4, 2>), dim3(grid), dim3(T::THREADS), 0, stream, p);
+    if (rest > 0)
+      hipLaunchKernelGGL((grad_weight_sums_kernel<F, T::BN, T::BK>), dim3(T::BN * T::BK / 1024, rest), dim3(256), 0, stream, p);
   };
-  using B = std::integral_constant<int, GRAD_BF16>;
-  using F = std::integral_constant<int, GRAD_F32>;
-  using P = std::integral_constant<int, GRAD_PART>;
-  if (g.splits > 1) {
-    go(P{});
-    const int64_t blocks = (N * (K / 4) + 255) / 256;
-    if (f32_out)
-      hipLaunchKernelGGL(grad_weight_sums_kernel<GRAD_F32>, dim3((unsigned)blocks), dim3(256), 0, stream, p);
+  auto size = [&](auto f) {
+    if (g.size == 256)
+      go(f, std::integral_constant<int, 4>{}, std::integral_constant<int, 8>{});
     else
-      hipLaunchKernelGGL(grad_weight_sums_kernel<GRAD_BF16>, dim3((unsigned)blocks), dim3(256), 0, stream, p);
-  } else {
-    f32_out ? go(F{}) : go(B{});
-  }
+      go(f, std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
+  };
+  f32_out ? size(std::true_type{}) : size(std::false_type{});
   return hipGetLastError();
 }
 
