@@ -324,6 +324,7 @@ mxq_status layer_norm(const char* fn, const void* x, mxq_dtype dt, int64_t rows,
   p.units = (uint32_t)(cols / 8);
   p.w_f32 = w_dt == MXQ_F32 ? 1 : 0;
   p.eps = eps;
+  p.cols = (float)cols;
   p.inv_cols = 1.0f / (float)cols;
   return hip_status(fn, mxq::launch_layer_norm(p, dt == MXQ_F32, quant, stream));
 }

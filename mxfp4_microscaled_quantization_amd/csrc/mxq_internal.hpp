@@ -96,7 +96,8 @@ struct NormParams {
   int64_t rows, ld_x, ld_y, ld_kept;
   uint32_t units;
   int w_f32;
-  float eps, inv_cols;
+  int past;                // loads and stores past the caches (set by the launcher)
+  float eps, cols, inv_cols;
 };
 hipError_t launch_layer_norm(const NormParams& p, bool f32, bool quant, hipStream_t stream);
 

@@ -25,6 +25,14 @@ __device__ __forceinline__ void widen_unit(const Unit<F32>& u, float (&v)[8]) {
   }
 }
 
+// Hides from the compiler that a unit is what it was: it is then widened again where it is used, instead of
+// being held widened from one pass to the next.
+template <bool F32>
+__device__ __forceinline__ void forget_unit(Unit<F32>& u) {
+  asm volatile("" : "+v"(u.d[0]));
+  if constexpr (F32) asm volatile("" : "+v"(u.d[1]));
+}
+
 // Rounds once, to nearest even, where the output is bf16.  PAST: stored past the caches.
 template <bool F32, bool PAST>
 __device__ __forceinline__ void store_unit(void* y, int64_t elem, const float (&v)[8]) {
@@ -66,22 +74,63 @@ __device__ __forceinline__ unsigned max_abs8(const float (&v)[8]) {
   return m;
 }
 
-// Sum over each 16 lanes, or the 64 of a wave, the same bits in every lane.
-__device__ __forceinline__ float row16_sum(float v) {
+// Sum over each group of G lanes (8 to 64), the same bits in every lane: DPP inside a row of 16, then
+// swaps of rows and of halves of the wave.
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
   auto dpp = [](float x, auto ctrl) {
     return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), decltype(ctrl)::value, 0xF, 0xF, false));
   };
   v += dpp(v, std::integral_constant<int, 0xB1>{});    // lane ^ 1
   v += dpp(v, std::integral_constant<int, 0x4E>{});    // lane ^ 2
   v += dpp(v, std::integral_constant<int, 0x141>{});   // row_half_mirror: the other quad of 8
-  v += dpp(v, std::integral_constant<int, 0x140>{});   // row_mirror: the other 8 of 16
+  if constexpr (G >= 16) v += dpp(v, std::integral_constant<int, 0x140>{});   // row_mirror: the other 8 of 16
+  if constexpr (G >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if constexpr (G >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
   return v;
 }
-__device__ __forceinline__ float wave_sum(float v) {
-  v = row16_sum(v);
-  v += __shfl_xor(v, 16);
-  v += __shfl_xor(v, 32);
+__device__ __forceinline__ float wave_sum(float v) { return group_sum<64>(v); }
+
+// Max over each group of G lanes, in every lane.
+template <int G>
+__device__ __forceinline__ unsigned group_max(unsigned v) {
+  v = G >= 16 ? row16_max_u32(v) : row8_max_u32(v);
+  if constexpr (G >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max(r[0], r[1]);
+  }
+  if constexpr (G >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = max(r[0], r[1]);
+  }
   return v;
+}
+
+// Sum of a unit's elements onto s.  Two bf16 in one instruction, which flushes subnormal numbers.
+template <bool F32>
+__device__ __forceinline__ float sum_unit(const Unit<F32>& u, float s) {
+  if constexpr (F32) {
+    float v[8];
+    widen_unit<true>(u, v);
+    return s + (((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7])));
+  } else {
+    const bf16x2 one = __builtin_bit_cast(bf16x2, 0x3F803F80u);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, u.d[0][k]), one, s, false);
+    return s;
+  }
+}
+
+// s / n, rounded correctly but for rare last bits, from inv = fl32(1 / n); exact where n divides s.
+__device__ __forceinline__ float quotient(float s, float n, float inv) {
+  const float q = s * inv;
+  return __builtin_fmaf(__builtin_fmaf(-q, n, s), inv, q);
 }
 
 }  // namespace mxq
