@@ -115,8 +115,9 @@ __global__ __launch_bounds__(C == 4 || (C == 2 && !ONE) ? 512 : 256) void layer_
         }
       }
     }
-    s1 = wave_sum(s1);
-    s2 = wave_sum(s2);
+    const float pair = wave_sum2(s1, s2);
+    s1 = of_lane(pair, 0);
+    s2 = of_lane(pair, 32);
     // quotients, not products with a rounded 1 / n: a row of equal values then has deviations of exactly 0
     const float e = quotient(s1, n, inv_n), q = __builtin_fmaf(-s1, e, s2);
     unsigned top = 0;
@@ -284,10 +285,13 @@ template <bool F32> struct Kept<F32, true> { v2u u; };
 // R rows at once.  AFFINE: with weights, and their sums.
 template <bool F32, bool CODES, bool AFFINE, int U, int R>
 __global__ __launch_bounds__(kNormThreads) void layer_norm_backward_kernel(NormGradParams p) {
-  __shared__ float red[2][R][2][16];
-  const uint32_t tid = threadIdx.x, T = blockDim.x, lane = tid & 63, wave = tid >> 6, waves = T >> 6;
+  static_assert(R == 1 || R == 2, "the four rows of a wave's lanes hold the sums");
+  // two slots in turn: a wave may reach the next rows' store while another still reads
+  __shared__ float red[2][4][16];
+  const uint32_t tid = threadIdx.x, T = blockDim.x, lane = tid & 63;
+  const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(tid >> 6));
   // slots of waves that are not there stay zero
-  for (uint32_t i = tid; i < 2 * R * 2 * 16; i += T) (&red[0][0][0][0])[i] = 0.0f;
+  for (uint32_t i = tid; i < 2 * 4 * 16; i += T) (&red[0][0][0])[i] = 0.0f;
   float w[U][8], dw[U][8], db[U][8];
 #pragma unroll
   for (int c = 0; c < U; ++c) {
@@ -305,24 +309,24 @@ __global__ __launch_bounds__(kNormThreads) void layer_norm_backward_kernel(NormG
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int64_t row = min(r0 + r, p.rows - 1);
+      const char* dy_row = static_cast<const char*>(p.dy) + row * p.ld_dy * (F32 ? 4 : 2);
+      const char* x_row = static_cast<const char*>(p.x) + row * p.ld_x * (CODES ? 1 : F32 ? 4 : 2);
 #pragma unroll
       for (int c = 0; c < U; ++c) {
-        const uint32_t i = c * T + tid;
-        const int64_t col = (int64_t)min(i, p.units - 1) * 8;   // threads past the row: its last unit, not used
-        dy[r][c] = load_unit<F32, true>(p.dy, row * p.ld_dy + col);
+        const uint32_t i = min(c * T + tid, p.units - 1);   // threads past the row: its last unit, not used
+        dy[r][c] = load_unit<F32, true>(dy_row, i * 8);
         if constexpr (CODES)
-          x[r][c].u = __builtin_nontemporal_load(reinterpret_cast<const v2u*>(static_cast<const int8_t*>(p.x) + row * p.ld_x + col));
+          x[r][c].u = __builtin_nontemporal_load(reinterpret_cast<const v2u*>(x_row + i * 8));
         else
-          x[r][c].u = load_unit<F32, true>(p.x, row * p.ld_x + col);
+          x[r][c].u = load_unit<F32, true>(x_row, i * 8);
       }
       mean[r] = p.mean[row];
       rstd[r] = p.rstd[row];
       scale[r] = CODES ? p.x_scales[row] : 1.0f;
     }
-    float g[R][U][8], xh[R][U][8];
+    float g[R][U][8], xh[R][U][8], s1[2] = {0.0f, 0.0f}, s2[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float s1 = 0.0f, s2 = 0.0f;
       const bool there = r0 + r < p.rows;
 #pragma unroll
       for (int c = 0; c < U; ++c) {
@@ -332,17 +336,16 @@ __global__ __launch_bounds__(kNormThreads) void layer_norm_backward_kernel(NormG
           widen_codes(x[r][c].u, scale[r], xh[r][c]);
         else
           widen_unit<F32>(x[r][c].u, xh[r][c]);
-        const bool in = there && (uint32_t)(c * T) + tid < p.units;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           xh[r][c][e] = (xh[r][c][e] - mean[r]) * rstd[r];
           g[r][c][e] = AFFINE ? d[e] * w[c][e] : d[e];
         }
-        if (in) {
+        if (there && c * T + tid < p.units) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            s1 += g[r][c][e];
-            s2 = __builtin_fmaf(g[r][c][e], xh[r][c][e], s2);
+            s1[r] += g[r][c][e];
+            s2[r] = __builtin_fmaf(g[r][c][e], xh[r][c][e], s2[r]);
             if constexpr (AFFINE) {
               dw[c][e] = __builtin_fmaf(d[e], xh[r][c][e], dw[c][e]);
               db[c][e] += d[e];
@@ -350,25 +353,24 @@ __global__ __launch_bounds__(kNormThreads) void layer_norm_backward_kernel(NormG
           }
         }
       }
-      s1 = wave_sum(s1);
-      s2 = wave_sum(s2);
-      if (lane == 0) {
-        red[par][r][0][wave] = s1;
-        red[par][r][1][wave] = s2;
-      }
     }
+    // row 0 of the wave's lanes: g's sum of the first matrix row, 1: of the second, 2 and 3: those of g xh
+    const float sums = R == 2 ? wave_sum4(s1[0], s2[0], s1[1], s2[1]) : wave_sum2(s1[0], s2[0]);
+    if ((lane & 15) == 0) red[par][lane >> 4][wave] = sums;
     __syncthreads();
+    const float total = row16_sum(red[par][lane >> 4][lane & 15]) * p.inv_cols;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float c1 = group_sum<16>(red[par][r][0][lane & 15]) * p.inv_cols;
-      const float c2 = group_sum<16>(red[par][r][1][lane & 15]) * p.inv_cols;
+      const float c1 = of_lane(total, 16 * r), c2 = of_lane(total, 32 + 16 * r);
+      if (r0 + r >= p.rows) break;
+      char* dx_row = static_cast<char*>(p.dx) + (r0 + r) * p.ld_dx * (F32 ? 4 : 2);
 #pragma unroll
       for (int c = 0; c < U; ++c) {
         const uint32_t i = c * T + tid;
         float o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = rstd[r] * (g[r][c][e] - __builtin_fmaf(xh[r][c][e], c2, c1));
-        if (r0 + r < p.rows && i < p.units) store_unit<F32, true>(p.dx, (r0 + r) * p.ld_dx + (int64_t)i * 8, o);
+        if (i < p.units) store_unit<F32, true>(dx_row, i * 8, o);
       }
     }
   }
@@ -381,6 +383,92 @@ __global__ __launch_bounds__(kNormThreads) void layer_norm_backward_kernel(NormG
         store_unit<true, false>(gridDim.x > 1 ? part : p.dw, (int64_t)i * 8, dw[c]);
         store_unit<true, false>(gridDim.x > 1 ? part + (int64_t)p.units * 8 : p.db, (int64_t)i * 8, db[c]);
       }
+    }
+  }
+}
+
+// Rows of up to G units, 64 / G of them in a wave, R rows of each group in flight: lane l of a group has unit l
+// of all rows that its workgroup takes.
+template <bool F32, bool CODES, bool AFFINE, int G>
+__global__ __launch_bounds__(256) void layer_norm_backward_short_kernel(NormGradParams p) {
+  constexpr int PER = 256 / G, R = 2;   // rows of the workgroup at once, passes in flight
+  __shared__ float red[4][2][G * 8];
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = threadIdx.x % G;
+  const bool own = l < p.units;
+  float w[8], dw[8], db[8];
+  load_vector8(AFFINE && own ? p.w : nullptr, p.w_f32, l, 1.0f, w);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) dw[e] = db[e] = 0.0f;
+  for (int64_t r0 = (int64_t)blockIdx.x * (PER * R) + threadIdx.x / G; r0 < p.rows; r0 += (int64_t)gridDim.x * (PER * R)) {
+    Unit<F32> dy[R];
+    Kept<F32, CODES> x[R];
+    float mean[R], rstd[R], scale[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t row = min(r0 + r * PER, p.rows - 1), col = (int64_t)min(l, p.units - 1) * 8;
+      dy[r] = load_unit<F32, true>(p.dy, row * p.ld_dy + col);
+      if constexpr (CODES)
+        x[r].u = __builtin_nontemporal_load(reinterpret_cast<const v2u*>(static_cast<const int8_t*>(p.x) + row * p.ld_x + col));
+      else
+        x[r].u = load_unit<F32, true>(p.x, row * p.ld_x + col);
+      mean[r] = p.mean[row];
+      rstd[r] = p.rstd[row];
+      scale[r] = CODES ? p.x_scales[row] : 1.0f;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t row = r0 + r * PER;
+      const bool in = own && row < p.rows;
+      float d[8], xh[8], s1 = 0.0f, s2 = 0.0f;
+      widen_unit<F32>(dy[r], d);
+      if constexpr (CODES)
+        widen_codes(x[r].u, scale[r], xh);
+      else
+        widen_unit<F32>(x[r].u, xh);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        d[e] = in ? d[e] : 0.0f;
+        xh[e] = in ? (xh[e] - mean[r]) * rstd[r] : 0.0f;
+        if constexpr (AFFINE) {
+          dw[e] = __builtin_fmaf(d[e], xh[e], dw[e]);
+          db[e] += d[e];
+          d[e] *= w[e];
+        }
+        s1 += d[e];
+        s2 = __builtin_fmaf(d[e], xh[e], s2);
+      }
+      const float c1 = group_sum<G>(s1) * p.inv_cols, c2 = group_sum<G>(s2) * p.inv_cols;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[e] = rstd[r] * (d[e] - __builtin_fmaf(xh[e], c2, c1));
+      if (in) store_unit<F32, true>(p.dx, row * p.ld_dx + (int64_t)l * 8, d);
+    }
+  }
+  if constexpr (AFFINE) {
+    // lanes of one l in a wave, then the waves
+    auto over_groups = [](float v) {
+      if constexpr (G == 8) v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xF, 0xF, true));   // row_ror by 8
+      if constexpr (G <= 16) v = fold16(v, v);
+      if constexpr (G <= 32) v = fold32(v, v);
+      return v;
+    };
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float sw = over_groups(dw[e]), sb = over_groups(db[e]);
+      if (lane < G) {
+        red[wave][0][l * 8 + e] = sw;
+        red[wave][1][l * 8 + e] = sb;
+      }
+    }
+    __syncthreads();
+    const uint32_t n = p.units * 8;
+    float* part = p.part + (int64_t)blockIdx.x * 2 * n;
+    for (uint32_t i = threadIdx.x; i < 2 * n; i += 256) {
+      const uint32_t k = i >= n, c = i - k * n;
+      const float v = (red[0][k][c] + red[1][k][c]) + (red[2][k][c] + red[3][k][c]);
+      if (gridDim.x > 1)
+        part[i] = v;
+      else
+        (k ? p.db : p.dw)[c] = v;
     }
   }
 }
@@ -411,13 +499,32 @@ __global__ __launch_bounds__(1024) void layer_norm_sums_kernel(const float* part
   }
 }
 
-// Rows at once in a workgroup of the gradient, and workgroups.
-int grad_rows(int64_t rows) { return rows < 1024 ? 1 : 2; }
-int64_t grad_threads(int64_t units) { return units > kNormThreads ? kNormThreads : (units + 63) / 64 * 64; }
-int64_t grad_groups(int64_t rows, int64_t cols) {
-  const int64_t per_cu = 1024 / grad_threads(cols / 8) + 1, cap = 256 * (per_cu < 8 ? per_cu : 8);
-  const int64_t sets = (rows + grad_rows(rows) - 1) / grad_rows(rows);
-  return sets < cap ? sets : cap;
+// The gradient's launch.  Workgroups leave 2 C floats each, so that there are no more of them than the GPU runs at once,
+// and each has 8 rows or more where there are enough rows (4099 x 2064 binary32: 512 workgroups 26 us, 1024 33, 256 30;
+// 75600 x 5120 bf16 from codes: 512 328 us, 1024 392).
+struct GradLaunch {
+  int lanes;      // of a row in the short kernel, or 0
+  int threads;
+  int64_t groups;
+};
+GradLaunch grad_launch(int64_t rows, int64_t cols) {
+  const int64_t units = cols / 8;
+  GradLaunch g;
+  g.lanes = units <= 8 ? 8 : units <= 16 ? 16 : units <= 32 ? 32 : units <= 64 ? 64 : 0;
+  g.threads = g.lanes ? 256 : units > kNormThreads ? kNormThreads : (int)((units + 63) / 64 * 64);
+  const int64_t each = g.lanes ? 256 / g.lanes * 2 : 1, sets = (rows + each - 1) / each;
+  const int64_t full = 256 * (1280 / g.threads), some = rows / 8 > 64 ? rows / 8 : 64;
+  g.groups = sets < full ? sets : full;
+  if (g.groups > some) g.groups = some;
+  return g;
+}
+
+// Whether a workgroup takes two rows at once, with one barrier for both: where a row has few waves (60000 x 1040 bf16 from
+// codes: 75 us for 80), where the GPU holds but one workgroup on a CU (30000 x 8192: 226 us for 243), and for binary32
+// (75600 x 5120: 917 us for 956).  Not for the rows between, of which more fit the registers one by one (75600 x
+// 5120 bf16 from codes: 371 us for 328).
+bool two_rows(int64_t rows, int threads, bool f32) {
+  return rows >= 1024 && (f32 || threads <= 256 || threads > 768);
 }
 
 }  // namespace
@@ -470,7 +577,7 @@ hipError_t launch_layer_norm(const NormParams& args, bool f32, bool quant, hipSt
 }
 
 size_t layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
-  const int64_t groups = grad_groups(rows, cols);
+  const int64_t groups = grad_launch(rows, cols).groups;
   return groups > 1 ? (size_t)groups * 2 * (size_t)cols * sizeof(float) : 0;
 }
 
@@ -482,25 +589,27 @@ hipError_t launch_layer_norm_backward(const NormGradParams& p, bool f32, bool co
     hipLaunchKernelGGL(layer_norm_sums_kernel, dim3((unsigned)((2 * cols + 63) / 64)), dim3(1024), 0, stream, p.part, 0, (uint32_t)cols, p.dw, p.db);
     return hipGetLastError();
   }
-  const unsigned groups = (unsigned)grad_groups(p.rows, cols), threads = (unsigned)grad_threads(p.units);
-  auto go = [&](auto f, auto c, auto a, auto u) {
-    constexpr bool F = decltype(f)::value, K = decltype(c)::value, A = decltype(a)::value;
-    constexpr int U = decltype(u)::value;
-    if constexpr (U == 1) {
-      if (grad_rows(p.rows) == 2) {
-        hipLaunchKernelGGL((layer_norm_backward_kernel<F, K, A, U, 2>), dim3(groups), dim3(threads), 0, stream, p);
-        return;
-      }
-    }
-    hipLaunchKernelGGL((layer_norm_backward_kernel<F, K, A, U, 1>), dim3(groups), dim3(threads), 0, stream, p);
-  };
+  const GradLaunch g = grad_launch(p.rows, cols);
+  const unsigned groups = (unsigned)g.groups;
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(groups), dim3((unsigned)g.threads), 0, stream, p); };
   using T = std::true_type;
   using N = std::false_type;
   auto u = [&](auto f, auto c, auto a) {
-    if (p.units <= kNormThreads)
-      go(f, c, a, std::integral_constant<int, 1>{});
+    constexpr bool F = decltype(f)::value, K = decltype(c)::value, A = decltype(a)::value;
+    if (g.lanes == 8)
+      go(layer_norm_backward_short_kernel<F, K, A, 8>);
+    else if (g.lanes == 16)
+      go(layer_norm_backward_short_kernel<F, K, A, 16>);
+    else if (g.lanes == 32)
+      go(layer_norm_backward_short_kernel<F, K, A, 32>);
+    else if (g.lanes == 64)
+      go(layer_norm_backward_short_kernel<F, K, A, 64>);
+    else if (p.units > kNormThreads)
+      go(layer_norm_backward_kernel<F, K, A, 2, 1>);
+    else if (two_rows(p.rows, g.threads, F))
+      go(layer_norm_backward_kernel<F, K, A, 1, 2>);
     else
-      go(f, c, a, std::integral_constant<int, 2>{});
+      go(layer_norm_backward_kernel<F, K, A, 1, 1>);
   };
   auto a = [&](auto f, auto c) { affine ? u(f, c, T{}) : u(f, c, N{}); };
   auto c = [&](auto f) { codes ? a(f, T{}) : a(f, N{}); };

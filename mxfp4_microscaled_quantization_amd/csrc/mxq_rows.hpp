@@ -74,28 +74,58 @@ __device__ __forceinline__ unsigned max_abs8(const float (&v)[8]) {
   return m;
 }
 
-// Sum over each group of G lanes (8 to 64), the same bits in every lane: DPP inside a row of 16, then
-// swaps of rows and of halves of the wave.
-template <int G>
-__device__ __forceinline__ float group_sum(float v) {
+// Sum over each row of 16 lanes, the same bits in every lane.
+__device__ __forceinline__ float row16_sum(float v) {
   auto dpp = [](float x, auto ctrl) {
-    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), decltype(ctrl)::value, 0xF, 0xF, false));
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), decltype(ctrl)::value, 0xF, 0xF, true));
   };
   v += dpp(v, std::integral_constant<int, 0xB1>{});    // lane ^ 1
   v += dpp(v, std::integral_constant<int, 0x4E>{});    // lane ^ 2
   v += dpp(v, std::integral_constant<int, 0x141>{});   // row_half_mirror: the other quad of 8
-  if constexpr (G >= 16) v += dpp(v, std::integral_constant<int, 0x140>{});   // row_mirror: the other 8 of 16
-  if constexpr (G >= 32) {
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  }
-  if constexpr (G >= 64) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  }
+  v += dpp(v, std::integral_constant<int, 0x140>{});   // row_mirror: the other 8 of 16
   return v;
 }
+
+// Lane i of the lower half gets a[i] + a[i + 32], lane i of the upper one b[i] + b[i - 32].
+__device__ __forceinline__ float fold32(float a, float b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// The same with rows of 16 lanes: rows 0 and 2 get a of their own and of the next row, rows 1 and 3 b of the row before
+// and of their own.
+__device__ __forceinline__ float fold16(float a, float b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Sum over each group of G lanes (8 to 64), the same bits in every lane of it.
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+  static_assert(G >= 8, "whole halves of rows");
+  if constexpr (G >= 64) v = fold32(v, v);
+  if constexpr (G >= 32) v = fold16(v, v);
+  if constexpr (G >= 16) return row16_sum(v);
+  auto dpp = [](float x, auto ctrl) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), decltype(ctrl)::value, 0xF, 0xF, true));
+  };
+  v += dpp(v, std::integral_constant<int, 0xB1>{});
+  v += dpp(v, std::integral_constant<int, 0x4E>{});
+  return v + dpp(v, std::integral_constant<int, 0x141>{});
+}
 __device__ __forceinline__ float wave_sum(float v) { return group_sum<64>(v); }
+
+// Sums over the wave of two values: a's in the lower half's lanes, b's in the upper half's.
+__device__ __forceinline__ float wave_sum2(float a, float b) {
+  const float t = fold32(a, b);
+  return row16_sum(fold16(t, t));
+}
+// Of four: a's in row 0 of 16 lanes, c's in row 1, b's in row 2, d's in row 3.
+__device__ __forceinline__ float wave_sum4(float a, float b, float c, float d) { return row16_sum(fold16(fold32(a, b), fold32(c, d))); }
+
+// Lane `lane` of v, as a scalar.
+__device__ __forceinline__ float of_lane(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
 
 // Max over each group of G lanes, in every lane.
 template <int G>
