@@ -52,12 +52,36 @@ __device__ __forceinline__ float act_slope(float u) {
   return __builtin_fmaf(t * (e * s), s, s);
 }
 
+// Largest |v| by a floating maximum, which passes over a NaN.  The values are finite where u is (|f(u)| <= |u|), and a row
+// whose u is not is told by u's own maximum.
+__device__ __forceinline__ float max8(float m, const float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) m = fmaxf(fmaxf(m, fabsf(v[e])), fabsf(v[e + 1]));
+  return m;
+}
+
+// The scale of the checkpoint of a row whose largest |u| has the pattern `top`: an infinity is clamped like any large
+// value, a NaN makes the scale NaN.
+template <int ACT>
+__device__ __forceinline__ Int8Scale checkpoint_scale(unsigned top) {
+  return int8_scale(top > 0x7F800000u ? top : min(top, __float_as_uint(checkpoint_limit<ACT>())));
+}
+
+template <bool F32, int ACT>
+__device__ __forceinline__ v2u checkpoint_codes(const Unit<F32>& u, const Int8Scale& sc) {
+  constexpr float kLimit = checkpoint_limit<ACT>();
+  float v[8];
+  widen_unit<F32>(u, v);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = __builtin_amdgcn_fmed3f(v[e], -kLimit, kLimit);
+  return pack_codes(v, sc);
+}
+
 // W waves for a row, C units of 8 elements in each thread; W == 1: four rows in a workgroup.
 template <bool F32, bool STREAM, bool QUANT, int ACT, int W, int C>
 __global__ __launch_bounds__(64 * (W < 4 ? 4 : W)) void activation_kernel(ActParams p) {
   constexpr int T = 64 * W, RPB = W < 4 ? 4 / W : 1;
   static_assert(W == 1 || W >= 4, "a workgroup holds whole rows");
-  constexpr float kLimit = checkpoint_limit<ACT>();
   __shared__ unsigned tops[2][2][W];
   const uint32_t tid = threadIdx.x % T, sub = threadIdx.x / T, lane = threadIdx.x & 63, wave = tid >> 6;
   int par = 0;
@@ -69,6 +93,7 @@ __global__ __launch_bounds__(64 * (W < 4 ? 4 : W)) void activation_kernel(ActPar
       u[c] = i < p.units ? load_unit<F32, STREAM>(p.u, row * p.ld_u + (int64_t)i * 8) : zero_unit<F32>();
     }
     unsigned top_u = 0, top_y = 0;
+    float most = 0.0f;
     float y[QUANT ? C : 1][8];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -78,14 +103,15 @@ __global__ __launch_bounds__(64 * (W < 4 ? 4 : W)) void activation_kernel(ActPar
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] = act<ACT>(o[e]);
       if constexpr (QUANT)
-        top_y = max(top_y, max_abs8(o));
+        most = max8(most, o);
       else if (i < p.units)
         store_unit<F32, STREAM>(p.y, row * p.ld_y + (int64_t)i * 8, o);
-      if (p.kept) top_u = max(top_u, unit_max<F32>(u[c]));
+      top_u = max(top_u, unit_max<F32>(u[c]));
     }
     if (QUANT || p.kept) {
-      if constexpr (QUANT) top_y = wave_max_u32(top_y);
-      if (p.kept) top_u = wave_max_u32(top_u);
+      top_y = __float_as_uint(most);
+      if constexpr (QUANT) top_y = group_max<64>(top_y);
+      top_u = group_max<64>(top_u);
       if constexpr (W > 1) {
         // two slots in turn: a wave may reach the next row's store while another still reads
         if (lane == 0) {
@@ -101,7 +127,7 @@ __global__ __launch_bounds__(64 * (W < 4 ? 4 : W)) void activation_kernel(ActPar
       }
     }
     if constexpr (QUANT) {
-      const Int8Scale sc = int8_scale(top_y);
+      const Int8Scale sc = int8_scale(top_u < 0x7F800000u ? top_y : top_u);
       if (tid == 0) p.scales[row] = sc.s;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
@@ -112,19 +138,54 @@ __global__ __launch_bounds__(64 * (W < 4 ? 4 : W)) void activation_kernel(ActPar
       }
     }
     if (p.kept) {
-      // an infinity is clamped like any large value; a NaN makes the row's scale NaN
-      const Int8Scale sc = int8_scale(top_u > 0x7F800000u ? top_u : min(top_u, __float_as_uint(kLimit)));
+      const Int8Scale sc = checkpoint_scale<ACT>(top_u);
       if (tid == 0) p.kept_scales[row] = sc.s;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const uint32_t i = c * T + tid;
-        if (i < p.units) {
-          float v[8];
-          widen_unit<F32>(u[c], v);
+        if (i < p.units)
+          __builtin_nontemporal_store(checkpoint_codes<F32, ACT>(u[c], sc), reinterpret_cast<v2u*>(p.kept + row * p.ld_kept + (int64_t)i * 8));
+      }
+    }
+  }
+}
+
+// Rows of up to G units, 64 / G of them in a wave: lane l of a group has unit l, R rows of each group in flight.
+template <bool F32, bool STREAM, bool QUANT, int ACT, int G>
+__global__ __launch_bounds__(256) void activation_short_kernel(ActParams p) {
+  constexpr int PER = 256 / G, R = 4;   // rows of the workgroup at once, passes in flight
+  const uint32_t l = threadIdx.x % G;
+  const bool own = l < p.units;
+  for (int64_t r0 = (int64_t)blockIdx.x * (PER * R) + threadIdx.x / G; r0 < p.rows; r0 += (int64_t)gridDim.x * (PER * R)) {
+    Unit<F32> u[R];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = __builtin_amdgcn_fmed3f(v[e], -kLimit, kLimit);
-          __builtin_nontemporal_store(pack_codes(v, sc), reinterpret_cast<v2u*>(p.kept + row * p.ld_kept + (int64_t)i * 8));
-        }
+    for (int k = 0; k < R; ++k) {
+      const int64_t row = r0 + k * PER;
+      u[k] = own && row < p.rows ? load_unit<F32, STREAM>(p.u, row * p.ld_u + (int64_t)l * 8) : zero_unit<F32>();
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const int64_t row = r0 + k * PER;
+      const bool in = own && row < p.rows;
+      const unsigned top_u = group_max<G>(unit_max<F32>(u[k]));
+      float o[8];
+      widen_unit<F32>(u[k], o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = act<ACT>(o[e]);
+      if constexpr (QUANT) {
+        const unsigned top_y = group_max<G>(__float_as_uint(max8(0.0f, o)));
+        const Int8Scale sc = int8_scale(top_u < 0x7F800000u ? top_y : top_u);
+        if (l == 0 && row < p.rows) p.scales[row] = sc.s;
+        if (in)
+          __builtin_nontemporal_store(pack_codes(o, sc), reinterpret_cast<v2u*>(static_cast<int8_t*>(p.y) + row * p.ld_y + (int64_t)l * 8));
+      } else if (in) {
+        store_unit<F32, STREAM>(p.y, row * p.ld_y + (int64_t)l * 8, o);
+      }
+      if (p.kept) {
+        const Int8Scale sc = checkpoint_scale<ACT>(top_u);
+        if (l == 0 && row < p.rows) p.kept_scales[row] = sc.s;
+        if (in)
+          __builtin_nontemporal_store(checkpoint_codes<F32, ACT>(u[k], sc), reinterpret_cast<v2u*>(p.kept + row * p.ld_kept + (int64_t)l * 8));
       }
     }
   }
@@ -177,18 +238,37 @@ hipError_t launch_activation(const ActParams& p, bool f32, bool quant, ActKind a
   auto pick = [&](auto f_tag, auto s_tag, auto q_tag, auto a_tag) {
     constexpr bool F = decltype(f_tag)::value, S = decltype(s_tag)::value, Q = decltype(q_tag)::value;
     constexpr int A = decltype(a_tag)::value;
-    if (p.units <= 64)
+    if (p.units <= 8)
+      go(activation_short_kernel<F, S, Q, A, 8>, 256, 32 * 4);
+    else if (p.units <= 16)
+      go(activation_short_kernel<F, S, Q, A, 16>, 256, 16 * 4);
+    else if (p.units <= 32)
+      go(activation_short_kernel<F, S, Q, A, 32>, 256, 8 * 4);
+    else if (p.units <= 64)
       go(activation_kernel<F, S, Q, A, 1, 1>, 256, 4);
     else if (p.units <= 128)
       go(activation_kernel<F, S, Q, A, 1, 2>, 256, 4);
+    else if (p.units <= 192)
+      go(activation_kernel<F, S, Q, A, 1, 3>, 256, 4);
     else if (p.units <= 256)
       go(activation_kernel<F, S, Q, A, 1, 4>, 256, 4);
     else if (p.units <= 256 * 2)
       go(activation_kernel<F, S, Q, A, 4, 2>, 256, 1);
+    else if (p.units <= 256 * 3)
+      go(activation_kernel<F, S, Q, A, 4, 3>, 256, 1);
     else if (p.units <= 256 * 4)
       go(activation_kernel<F, S, Q, A, 4, 4>, 256, 1);
-    else if (p.units <= 512 * 4)
-      go(activation_kernel<F, S, Q, A, 8, 4>, 512, 1);
+    else if (p.units <= 512 * 3)
+      go(activation_kernel<F, S, Q, A, 8, 3>, 512, 1);
+    else if (p.units <= 1024 * 2) {
+      // a row's values stay in registers where they become codes: fewer and longer threads then (75600 x 13824 bf16 to
+      // codes: 591 us, over 16 waves 872; to bf16 with a checkpoint 914 and 897)
+      if constexpr (Q)
+        go(activation_kernel<F, S, Q, A, 8, 4>, 512, 1);
+      else
+        go(activation_kernel<F, S, Q, A, 16, 2>, 1024, 1);
+    } else if (p.units <= 1024 * 4)
+      go(activation_kernel<F, S, Q, A, 16, 4>, 1024, 1);
     else
       go(activation_kernel<F, S, Q, A, 16, 8>, 1024, 1);
   };
