@@ -553,7 +553,7 @@ mxq_status mxq_activation_backward(const void* dy, mxq_dtype dt, int64_t rows, i
  * sum is added to what `out` holds, in binary32, before the rounding.
  * The order of the sum is decided by M, N and K alone: the same inputs give the same bits.
  * dy      : M x N bf16, pitch ld_dy elements below 2^23; base and pitch 16-byte aligned.
- * codes   : M x K int8, pitch ld_codes bytes; base and pitch multiples of 16.  scales : float[M].
+ * codes   : M x K int8, pitch ld_codes bytes below 2^23; base and pitch multiples of 16.  scales : float[M].
  * out     : N x K of out_dt, pitch ld_out elements (>= K), naturally aligned (stored fastest on 16-byte
  *           boundaries).
  * N % 8 == 0, K % 16 == 0; N and K up to 2^22, N * K up to 2^36, M * K below 2^35.  M == 0 gives zeros

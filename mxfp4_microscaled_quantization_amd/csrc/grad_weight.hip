@@ -4,7 +4,8 @@
 // error 2^-9 at most, beside the half step of the codes themselves) is the one of
 // mxq_dequantize_int8: the matrix cores take it as an operand, and the products are exact.
 //
-// The codes are widened into a workspace first.  The product contracts over rows of both
+// The largest tile takes values that a launch ahead of it has widened into a workspace (its registers are full, and each
+// code meets many tiles); the smaller one widens the codes on their way into LDS.  The product contracts over rows of both
 // operands, while an MFMA takes 8 consecutive values of the contraction in a lane: fragments
 // come from LDS by ds_read_b64_tr_b16, in which 16 lanes read 4 rows of 16 columns and each
 // gets the 4 values of one column.
@@ -21,7 +22,10 @@ constexpr int kWinRows = 64;   // rows of both operands in LDS at once: two MFMA
 
 struct GradParams {
   const uint16_t* dy;
-  const uint16_t* x;
+  const uint16_t* x;        // the codes' values, or (CODES)
+  const int8_t* codes;      // the codes themselves
+  const float* scales;
+  int64_t ld_codes;
   void* out;
   float* part;              // sums of the parts of M, [tile - whole][splits][rows of a tile][columns]
   int64_t ld_dy, ld_x, ld_out;
@@ -115,12 +119,13 @@ __device__ __forceinline__ void grad_region(std::integer_sequence<int, Is...>) {
   (grad_region_unit<ID, R, MFMAS, VM, Is>(), ...);
 }
 
-template <bool F32OUT, int MI, int MJ, int WK, int WN>
+// CODES: the codes are loaded and widened into the ring by the kernel itself.
+template <bool F32OUT, bool CODES, int MI, int MJ, int WK, int WN>
 __global__ __launch_bounds__(64 * WK * WN, 1) void grad_weight_kernel(GradParams p) {
   using T = GradTile<MI, MJ, WK, WN>;
   constexpr int WAVES = WK * WN, NX = 2, NY = 3;   // ring depths
   constexpr int LX = (int)(T::X_TILE / 1024) / WAVES, LY = (int)(T::Y_TILE / 1024) / WAVES;   // 1 KB lines per wave
-  constexpr int RD = MI + MJ, VM = LX + LY;
+  constexpr int RD = MI + MJ, DX = CODES ? 0 : LX, VM = DX + LY;   // loads into LDS for each window
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NX * T::X_TILE + NY * T::Y_TILE];
   constexpr uint32_t Y_BASE = NX * T::X_TILE;
 
@@ -172,6 +177,35 @@ __global__ __launch_bounds__(64 * WK * WN, 1) void grad_weight_kernel(GradParams
   auto issue_y = [&](__amdgpu_buffer_rsrc_t r, uint32_t slot, int j) {
     fill(r, lds + Y_BASE + slot * T::Y_TILE, (uint32_t)p.ld_dy, wave * LY + j, std::integral_constant<uint32_t, T::BN>{});
   };
+  // CODES: thread t widens 16 codes of row t / (BK / 16) of a window, one 32-byte unit
+  constexpr uint32_t TPR = T::BK / 16;
+  static_assert(!CODES || TPR * kWinRows == 64 * WAVES, "one unit for each thread");
+  const uint32_t crow = tid / TPR, cunit = tid % TPR;
+  struct Raw {
+    v4u c;
+    float s;
+  };
+  auto load_codes = [&](int w) {
+    const int rows = max(0, min(m_hi - w * kWinRows, kWinRows)), ld = (int)p.ld_codes;
+    const int bytes = scalar(max(rows * ld - (ld - (p.K - k0)), 0));
+    const __amdgpu_buffer_rsrc_t rc = make_rsrc(p.codes + (int64_t)w * kWinRows * ld + k0, (uint32_t)bytes);
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(p.scales + (int64_t)w * kWinRows, (uint32_t)scalar(rows) * 4u);
+    Raw r;   // rows past the end: zeros
+    r.c = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rc, crow * ld + cunit * 16, 0, 0));
+    r.s = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, crow * 4, 0, 0));
+    return r;
+  };
+  auto store_codes = [&](const Raw& r, uint32_t slot) {
+    uint8_t* to = lds + slot * T::X_TILE + crow * (T::BK * 2) + ((cunit ^ (crow & 7)) << 5);
+    unsigned o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int pair = (int)(r.c[e >> 1] >> (16 * (e & 1)));
+      o[e] = pack_bf16x2((float)(int8_t)pair * r.s, (float)(int8_t)(pair >> 8) * r.s);
+    }
+    *reinterpret_cast<v4u*>(to) = v4u{o[0], o[1], o[2], o[3]};
+    *reinterpret_cast<v4u*>(to + 16) = v4u{o[4], o[5], o[6], o[7]};
+  };
   // the fragment of 16 columns from unit u, tokens 32 t + 4 g + (0 .. 3) and 16 more, g = lane / 16
   const uint32_t q = lane & 15, row0 = 4 * (lane >> 4) + (q >> 2);
   const uint32_t at_x = row0 * (T::BK * 2) + ((row0 & 7) << 5) + 8 * (q & 3), at_y = row0 * (T::BN * 2) + ((row0 & 7) << 5) + 8 * (q & 3);
@@ -215,45 +249,59 @@ __global__ __launch_bounds__(64 * WK * WN, 1) void grad_weight_kernel(GradParams
     asm volatile("" ::: "memory");
   };
 
-  // prologue: window w_lo resident; then, in the order the steady state issues them, x of the next window, and dy of
-  // the next two (y of w+1 first: the hand-over leaves only the last in flight)
+  // prologue: window w_lo resident; then, in the order the steady state issues them, dy of the next window, x of it, and
+  // dy of the one after (the hand-over leaves only the last in flight; CODES: and the codes behind it)
   v4u f0[RD], f1[RD];
+  Raw raw;
   if (w_lo < w_hi) {
+    if constexpr (CODES) {
+      store_codes(load_codes(w_lo), 0);
+    } else {
 #pragma unroll
-    for (int j = 0; j < LX; ++j) issue_x(x_rows(w_lo), 0, j);
+      for (int j = 0; j < LX; ++j) issue_x(x_rows(w_lo), 0, j);
+    }
 #pragma unroll
     for (int j = 0; j < LY; ++j) issue_y(y_rows(w_lo), 0, j);
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < LY; ++j) issue_y(y_rows(w_lo + 1), 1, j);
+    if constexpr (CODES) {
+      raw = load_codes(w_lo + 1);
+    } else {
 #pragma unroll
-    for (int j = 0; j < LX; ++j) issue_x(x_rows(w_lo + 1), 1, j);
+      for (int j = 0; j < LX; ++j) issue_x(x_rows(w_lo + 1), 1, j);
+    }
 #pragma unroll
     for (int j = 0; j < LY; ++j) issue_y(y_rows(w_lo + 2), 2, j);
     read(f0, 0, 0, 0, [](int) {});
   }
   // One window: step 0 on f0 under the reads of step 1 into f1; the hand-over waits for window w+1 (only dy of window
   // w+2 may still be in flight) and releases window w's slots; step 1 on f1 under the reads of window w+1's step 0 and the
-  // loads of x of window w+2 and dy of window w+3 into those slots.
+  // loads of x of window w+2 and dy of window w+3 into those slots.  CODES: x of window w+1 is written ahead of the
+  // hand-over, into the slot that the last one released, and the codes of window w+2 are loaded behind it.
   uint32_t sx = 0, sy = 0;
   for (int w = w_lo; w < w_hi; ++w) {
     const __amdgpu_buffer_rsrc_t rx = x_rows(w + NX), ry = y_rows(w + NY);
     const uint32_t sx1 = sx ^ 1, sy1 = sy == NY - 1 ? 0 : sy + 1;
     read(f1, sx, sy, 1, [](int) {});
+    if constexpr (CODES) {
+      store_codes(raw, sx1);
+      raw = load_codes(w + 2);
+    }
     step(f0);
-    grad_region<0, RD, MI * MJ, 0>(std::make_integer_sequence<int, RD>{});
+    if constexpr (!CODES) grad_region<0, RD, MI * MJ, 0>(std::make_integer_sequence<int, RD>{});
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(grad_wait_vm(LY));
+    __builtin_amdgcn_s_waitcnt(grad_wait_vm(CODES ? LY + 2 : LY));
     barrier();
     __builtin_amdgcn_sched_barrier(0);
     read(f0, sx1, sy1, 0, [&](int k) {
       if (grad_loads_after(k, VM, RD) > 0) {
         const int j = k * VM / RD;
-        if (j < LX)
+        if (j < DX)
           issue_x(rx, sx, j);
         else
-          issue_y(ry, sy, j - LX);
+          issue_y(ry, sy, j - DX);
       }
     });
     step(f1);
@@ -307,15 +355,16 @@ GradPlan plan_grad(int64_t M, int64_t N, int64_t K) {
   const int nwin = (int)((M + kWinRows - 1) / kWinRows);
   for (const int size : {256, 128}) {
     const int64_t slots = size == 256 ? 256 : 512;                  // workgroups at once
-    const double window = size == 256 ? 1.9 : 1.25, ends = 6.0;     // of a workgroup on a full GPU
+    const double window = size == 256 ? 1.65 : 1.15, ends = 6.0;    // of a workgroup on a full GPU
     const int64_t tn = (N + size - 1) / size, tk = (K + size - 1) / size, tiles = tn * tk;
     const int64_t whole = tiles / slots * slots, rest = tiles - whole;
-    const double base = (double)(whole / slots) * (nwin * window + ends);
+    // the largest tile's operand is widened by a launch of its own
+    const double base = (double)(whole / slots) * (nwin * window + ends) + (size == 256 ? 4.0 + (double)M * K * 3 / 5.5e6 : 0.0);
     for (int s = 1; s == 1 || (s * 2 <= nwin && rest * s <= 4 * slots); ++s) {
       double t = base;
       if (rest > 0) {
         t += (double)((rest * s + slots - 1) / slots) * ((nwin + s - 1) / s * window + ends);
-        if (s > 1) t += 5.0 + (double)(rest * s * size * size) * 8.0 / 4e6;
+        if (s > 1) t += 5.0 + (double)(rest * s * size * size) * 8.0 / 5.5e6;
       }
       if (least == 0.0 || t < least) {
         least = t;
@@ -327,13 +376,16 @@ GradPlan plan_grad(int64_t M, int64_t N, int64_t K) {
   return best;
 }
 
-size_t round256(size_t v) { return (v + 255) / 256 * 256; }
+// The values of the codes, where they are widened ahead of the product.
+size_t values_bytes(const GradPlan& g, int64_t M, int64_t K) {
+  return g.size == 256 ? ((size_t)M * (size_t)K * 2 + 255) / 256 * 256 : 0;
+}
 
 }  // namespace
 
 size_t grad_weight_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   const GradPlan g = plan_grad(M, N, K);
-  return round256((size_t)M * (size_t)K * 2) + (size_t)(g.tiles_n * g.tiles_k - g.whole) * g.splits * g.size * g.size * 4;
+  return values_bytes(g, M, K) + (size_t)(g.tiles_n * g.tiles_k - g.whole) * g.splits * g.size * g.size * 4;
 }
 
 hipError_t launch_grad_weight_int8(const uint16_t* dy, int64_t ld_dy, const int8_t* codes, int64_t ld_codes,
@@ -342,13 +394,18 @@ hipError_t launch_grad_weight_int8(const uint16_t* dy, int64_t ld_dy, const int8
   if (N == 0 || K == 0 || (M == 0 && accumulate)) return hipSuccess;
   const GradPlan g = plan_grad(M, N, K);
   uint16_t* x = static_cast<uint16_t*>(workspace);
-  const hipError_t e = launch_dequantize_int8(codes, ld_codes, scales, M, K, x, K, stream);
-  if (e != hipSuccess) return e;
+  if (g.size == 256) {
+    const hipError_t e = launch_dequantize_int8(codes, ld_codes, scales, M, K, x, K, stream);
+    if (e != hipSuccess) return e;
+  }
   GradParams p;
   p.dy = dy;
   p.x = x;
+  p.codes = codes;
+  p.scales = scales;
+  p.ld_codes = ld_codes;
   p.out = out;
-  p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + round256((size_t)M * (size_t)K * 2));
+  p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + values_bytes(g, M, K));
   p.ld_dy = ld_dy;
   p.ld_x = K;
   p.ld_out = ld_out;
@@ -365,19 +422,19 @@ hipError_t launch_grad_weight_int8(const uint16_t* dy, int64_t ld_dy, const int8
   p.vec = reinterpret_cast<uintptr_t>(out) % (4 * step) == 0 && ld_out % 4 == 0;
   const int rest = g.tiles_n * g.tiles_k - g.whole;
   const unsigned grid = (unsigned)(g.whole + rest * g.splits);
-  auto go = [&](auto f_tag, auto mi_tag, auto mj_tag) {
-    constexpr bool F = decltype(f_tag)::value;
+  auto go = [&](auto f_tag, auto c_tag, auto mi_tag, auto mj_tag) {
+    constexpr bool F = decltype(f_tag)::value, C = decltype(c_tag)::value;
     constexpr int MI = decltype(mi_tag)::value, MJ = decltype(mj_tag)::value;
     using T = GradTile<MI, MJ, 4, 2>;
-    hipLaunchKernelGGL((grad_weight_kernel<F, MI, MJ, 4, 2>), dim3(grid), dim3(T::THREADS), 0, stream, p);
+    hipLaunchKernelGGL((grad_weight_kernel<F, C, MI, MJ, 4, 2>), dim3(grid), dim3(T::THREADS), 0, stream, p);
     if (rest > 0)
       hipLaunchKernelGGL((grad_weight_sums_kernel<F, T::BN, T::BK>), dim3(T::BN * T::BK / 1024, rest), dim3(256), 0, stream, p);
   };
   auto size = [&](auto f) {
     if (g.size == 256)
-      go(f, std::integral_constant<int, 4>{}, std::integral_constant<int, 8>{});
+      go(f, std::false_type{}, std::integral_constant<int, 4>{}, std::integral_constant<int, 8>{});
     else
-      go(f, std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
+      go(f, std::true_type{}, std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
   };
   f32_out ? size(std::true_type{}) : size(std::false_type{});
   return hipGetLastError();

@@ -922,6 +922,7 @@ mxq_status mxq_grad_weight_int8(const uint16_t* dy, int64_t ld_dy, const int8_t*
   if (K % 16 != 0) return fail(MXQ_ERR_INVALID_ARG, "%s: K (%lld) must be a multiple of 16", fn, (long long)K);
   if (N > 0 && K > 0 && !grad_shape_ok(M, N, K)) return fail(MXQ_ERR_INVALID_ARG, "%s: problem too large", fn);
   if (ld_dy >= ((int64_t)1 << 23)) return fail(MXQ_ERR_INVALID_ARG, "%s: ld of dy (%lld) must be below 2^23", fn, (long long)ld_dy);
+  if (ld_codes >= ((int64_t)1 << 23)) return fail(MXQ_ERR_INVALID_ARG, "%s: ld of codes (%lld) must be below 2^23", fn, (long long)ld_codes);
   mxq_status st = check_plane(fn, "dy", dy, K > 0 ? M : 0, N, ld_dy, 2, 16);
   if (st != MXQ_OK) return st;
   if ((st = check_plane(fn, "codes", codes, N > 0 ? M : 0, K, ld_codes, 1, 16)) != MXQ_OK) return st;

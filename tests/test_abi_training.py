@@ -51,6 +51,7 @@ def _grad(dy=OK16, ldy=64, c=OK16, ldc=32, s=OK16, M=4, N=64, K=32, out=OK16, dt
 
 KEEP = dict(xc=OK16, ldxc=64, xs=OK16)
 CKPT = dict(uc=OK16, lduc=64, us=OK16)
+BIGGER = dict(M=3584, N=5120, K=5120, ldy=5120, ldc=5120, ldo=5120)   # with a workspace
 INVALID = [
     (_norm, dict(C=60, ld=64), "multiple of 8"), (_norm, dict(C=72, ld=72, ldy=72, xc=OK16, ldxc=80, xs=OK16), "multiple of 16"),
     (_norm, dict(C=0), "cols"), (_norm, dict(C=16392, ld=16392, ldy=16392), "cols"), (_norm, dict(T=-1), "negative"),
@@ -72,8 +73,8 @@ INVALID = [
     (_back, dict(dx=None), "dx is NULL"), (_back, dict(dx=ODD8), "dx base"), (_back, dict(lddx=68), "dx base"),
     (_back, dict(mean=None), "mean"), (_back, dict(rstd=None), "rstd"), (_back, dict(mean=ODD2), "mean"), (_back, dict(w=ODD8), "w and b"),
     (_back, dict(dw=None), "together"), (_back, dict(db=None), "together"), (_back, dict(dw=ODD8), "dw and db"),
-    (_back, dict(db=ODD2), "dw and db"), (_back, dict(ws=None), "workspace"), (_back, dict(ws=ODD8), "workspace"),
-    (_back, dict(nbytes=100), "workspace"),
+    (_back, dict(db=ODD2), "dw and db"), (_back, dict(T=4096, ws=None), "workspace"), (_back, dict(T=4096, ws=ODD8), "workspace"),
+    (_back, dict(T=4096, nbytes=100), "workspace"),
     (_act, dict(C=60), "multiple of 8"), (_act, CKPT | dict(C=72, ld=72, ldy=72, lduc=80), "multiple of 16"),
     (_act, dict(C=65544, ld=65544, ldy=65544), "at most"), (_act, dict(T=-1), "negative"), (_act, dict(u=None), "NULL"),
     (_act, dict(u=ODD8), "aligned"), (_act, dict(ld=56), "ld_x"), (_act, dict(y=None), "y is NULL"), (_act, dict(ldy=60), "ld of y"),
@@ -88,9 +89,9 @@ INVALID = [
     (_grad, dict(N=2 ** 23, ldy=2 ** 23 - 8), "too large"), (_grad, dict(K=2 ** 23, ldc=2 ** 23, ldo=2 ** 23), "too large"),
     (_grad, dict(N=2 ** 20, K=2 ** 20), "too large"), (_grad, dict(ldy=2 ** 23), "ld of dy"), (_grad, dict(ldy=56), "ld of dy"),
     (_grad, dict(ldy=68), "dy base"), (_grad, dict(dy=ODD8), "dy base"), (_grad, dict(dy=None), "dy is NULL"), (_grad, dict(c=None), "codes is NULL"),
-    (_grad, dict(c=ODD8), "codes base"), (_grad, dict(ldc=40), "codes base"), (_grad, dict(ldc=16), "ld of codes"), (_grad, dict(s=None), "scales"),
+    (_grad, dict(c=ODD8), "codes base"), (_grad, dict(ldc=40), "codes base"), (_grad, dict(ldc=16), "ld of codes"), (_grad, dict(ldc=2 ** 23), "ld of codes"), (_grad, dict(s=None), "scales"),
     (_grad, dict(s=ODD2), "scales"), (_grad, dict(out=None), "out is NULL"), (_grad, dict(out=ODD2), "out base"), (_grad, dict(ldo=31), "ld of out"),
-    (_grad, dict(ldo=BIG), "2^32"), (_grad, dict(ws=None), "workspace"), (_grad, dict(ws=ODD8), "workspace"), (_grad, dict(nbytes=16), "workspace"),
+    (_grad, dict(ldo=BIG), "2^32"), (_grad, BIGGER | dict(ws=None), "workspace"), (_grad, BIGGER | dict(ws=ODD8), "workspace"), (_grad, BIGGER | dict(nbytes=16), "workspace"),
 ]
 
 
@@ -127,7 +128,8 @@ def test_workspace_sizes():
     assert back(1, 5120) == 0 and back(75600, 5120) > 0 and back(75600, 5120) < 75600 * 5120
     for M, N, K in ((-1, 8, 16), (4, 0, 16), (4, 8, 0), (4, 12, 16), (4, 8, 24), (2 ** 31, 8, 16), (4, 2 ** 23, 16)):
         assert grad(M, N, K) == 0
-    assert grad(0, 8, 16) == 0
+    assert grad(0, 8, 16) == 0 and grad(64, 64, 64) == 0
+    assert grad(3584, 5120, 5120) >= 3584 * 5120 * 2
 
 
 # ------------------------------------------------------------------ binding
