@@ -36,9 +36,10 @@ struct GradParams {
 };
 
 
-// MI x MJ fragments of 16 x 16 outputs (k, n) in a wave, WK x WN waves.
-template <int MI, int MJ, int WK, int WN>
+// MI x MJ fragments of 16 x 16 outputs (k, n) in a wave, WK x WN waves; rings of NX windows of x and NY of dy.
+template <int MI_, int MJ_, int WK_, int WN_, int NY_>
 struct GradTile {
+  static constexpr int MI = MI_, MJ = MJ_, WK = WK_, WN = WN_, NX = 2, NY = NY_;
   static constexpr int THREADS = 64 * WK * WN, BK = 16 * MI * WK, BN = 16 * MJ * WN;
   static constexpr uint32_t X_TILE = kWinRows * BK * 2, Y_TILE = kWinRows * BN * 2;
 };
@@ -104,6 +105,16 @@ constexpr int grad_wait_vm(int vm) { return (vm & 0xF) | ((vm >> 4) << 14) | (0x
 // which of n loads spread over rd reads go out right after read k
 constexpr int grad_loads_after(int k, int n, int rd) { return (k + 1) * n / rd - k * n / rd; }
 
+// f(0) && f(1) && ... && f(N - 1), the arguments as integral constants.
+template <class F, int... Is>
+__device__ __forceinline__ bool each_window_of(F&& f, std::integer_sequence<int, Is...>) {
+  return (f(std::integral_constant<int, Is>{}) && ...);
+}
+template <int N, class F>
+__device__ __forceinline__ bool each_window(F&& f) {
+  return each_window_of(f, std::make_integer_sequence<int, N>{});
+}
+
 // Scheduling pattern of one MFMA region: unit I is the two reads of a fragment, then the tile loads
 // that fall there, then its share of the region's MFMAs.
 template <int ID, int R, int MFMAS, int VM, int I>
@@ -120,10 +131,10 @@ __device__ __forceinline__ void grad_region(std::integer_sequence<int, Is...>) {
 }
 
 // CODES: the codes are loaded and widened into the ring by the kernel itself.
-template <bool F32OUT, bool CODES, int MI, int MJ, int WK, int WN>
-__global__ __launch_bounds__(64 * WK * WN, 1) void grad_weight_kernel(GradParams p) {
-  using T = GradTile<MI, MJ, WK, WN>;
-  constexpr int WAVES = WK * WN, NX = 2, NY = 3;   // ring depths
+template <bool F32OUT, bool CODES, class T>
+__global__ __launch_bounds__(T::THREADS, 2) void grad_weight_kernel(GradParams p) {
+  constexpr int MI = T::MI, MJ = T::MJ, WK = T::WK, WN = T::WN, WAVES = WK * WN, NX = T::NX, NY = T::NY;
+  constexpr int D = CODES ? NY - 1 : 1;   // windows of codes in registers, on their way
   constexpr int LX = (int)(T::X_TILE / 1024) / WAVES, LY = (int)(T::Y_TILE / 1024) / WAVES;   // 1 KB lines per wave
   constexpr int RD = MI + MJ, DX = CODES ? 0 : LX, VM = DX + LY;   // loads into LDS for each window
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NX * T::X_TILE + NY * T::Y_TILE];
@@ -177,13 +188,14 @@ __global__ __launch_bounds__(64 * WK * WN, 1) void grad_weight_kernel(GradParams
   auto issue_y = [&](__amdgpu_buffer_rsrc_t r, uint32_t slot, int j) {
     fill(r, lds + Y_BASE + slot * T::Y_TILE, (uint32_t)p.ld_dy, wave * LY + j, std::integral_constant<uint32_t, T::BN>{});
   };
-  // CODES: thread t widens 16 codes of row t / (BK / 16) of a window, one 32-byte unit
-  constexpr uint32_t TPR = T::BK / 16;
-  static_assert(!CODES || TPR * kWinRows == 64 * WAVES, "one unit for each thread");
+  // CODES: a thread widens units of 16 codes, of a row and of every ROWS-th one further, into 32 bytes each
+  constexpr uint32_t TPR = T::BK / 16, ROWS = 64 * WAVES / TPR;
+  constexpr int UPT = kWinRows / ROWS;
+  static_assert(!CODES || (UPT * ROWS == kWinRows && ROWS % 8 == 0), "whole rounds, and one swizzle for a thread's rows");
   const uint32_t crow = tid / TPR, cunit = tid % TPR;
   struct Raw {
-    v4u c;
-    float s;
+    v4u c[UPT];
+    float s[UPT];
   };
   auto load_codes = [&](int w) {
     const int rows = max(0, min(m_hi - w * kWinRows, kWinRows)), ld = (int)p.ld_codes;
@@ -191,20 +203,27 @@ __global__ __launch_bounds__(64 * WK * WN, 1) void grad_weight_kernel(GradParams
     const __amdgpu_buffer_rsrc_t rc = make_rsrc(p.codes + (int64_t)w * kWinRows * ld + k0, (uint32_t)bytes);
     const __amdgpu_buffer_rsrc_t rs = make_rsrc(p.scales + (int64_t)w * kWinRows, (uint32_t)scalar(rows) * 4u);
     Raw r;   // rows past the end: zeros
-    r.c = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rc, crow * ld + cunit * 16, 0, 0));
-    r.s = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, crow * 4, 0, 0));
+#pragma unroll
+    for (int j = 0; j < UPT; ++j) {
+      r.c[j] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rc, crow * ld + cunit * 16, j * ROWS * ld, 0));
+      r.s[j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, crow * 4, j * ROWS * 4, 0));
+    }
     return r;
   };
   auto store_codes = [&](const Raw& r, uint32_t slot) {
     uint8_t* to = lds + slot * T::X_TILE + crow * (T::BK * 2) + ((cunit ^ (crow & 7)) << 5);
-    unsigned o[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int pair = (int)(r.c[e >> 1] >> (16 * (e & 1)));
-      o[e] = pack_bf16x2((float)(int8_t)pair * r.s, (float)(int8_t)(pair >> 8) * r.s);
-    }
-    *reinterpret_cast<v4u*>(to) = v4u{o[0], o[1], o[2], o[3]};
-    *reinterpret_cast<v4u*>(to + 16) = v4u{o[4], o[5], o[6], o[7]};
+    for (int j = 0; j < UPT; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        v4u o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int pair = (int)(r.c[j][2 * h + (e >> 1)] >> (16 * (e & 1)));
+          o[e] = pack_bf16x2((float)(int8_t)pair * r.s[j], (float)(int8_t)(pair >> 8) * r.s[j]);
+        }
+        *reinterpret_cast<v4u*>(to + j * (ROWS * T::BK * 2) + 16 * h) = o;
+      }
   };
   // the fragment of 16 columns from unit u, tokens 32 t + 4 g + (0 .. 3) and 16 more, g = lane / 16
   const uint32_t q = lane & 15, row0 = 4 * (lane >> 4) + (q >> 2);
@@ -249,50 +268,61 @@ __global__ __launch_bounds__(64 * WK * WN, 1) void grad_weight_kernel(GradParams
     asm volatile("" ::: "memory");
   };
 
-  // prologue: window w_lo resident; then, in the order the steady state issues them, dy of the next window, x of it, and
-  // dy of the one after (the hand-over leaves only the last in flight; CODES: and the codes behind it)
+  // prologue: the loads of window w_lo and, in the order of the steady state, of the next windows; then w_lo resident
   v4u f0[RD], f1[RD];
-  Raw raw;
+  Raw raw[D];   // CODES: window w's in raw[(w - w_lo) % D]
   if (w_lo < w_hi) {
+    Raw first;
     if constexpr (CODES) {
-      store_codes(load_codes(w_lo), 0);
+      first = load_codes(w_lo);
     } else {
 #pragma unroll
       for (int j = 0; j < LX; ++j) issue_x(x_rows(w_lo), 0, j);
     }
 #pragma unroll
     for (int j = 0; j < LY; ++j) issue_y(y_rows(w_lo), 0, j);
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);   // the waits count on this order
 #pragma unroll
-    for (int j = 0; j < LY; ++j) issue_y(y_rows(w_lo + 1), 1, j);
-    if constexpr (CODES) {
-      raw = load_codes(w_lo + 1);
-    } else {
+    for (int k = 1; k < NY; ++k) {
+      if constexpr (CODES) {
+        raw[k % D] = load_codes(w_lo + k);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (!CODES && k == NY - 1)
 #pragma unroll
-      for (int j = 0; j < LX; ++j) issue_x(x_rows(w_lo + 1), 1, j);
+        for (int j = 0; j < LX; ++j) issue_x(x_rows(w_lo + 1), 1, j);
+#pragma unroll
+      for (int j = 0; j < LY; ++j) issue_y(y_rows(w_lo + k), k, j);
+      __builtin_amdgcn_sched_barrier(0);
     }
-#pragma unroll
-    for (int j = 0; j < LY; ++j) issue_y(y_rows(w_lo + 2), 2, j);
+    if constexpr (CODES) store_codes(first, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(grad_wait_vm((NY - 1) * LY + (CODES ? (NY - 1) * 2 * UPT : LX)));
+    barrier();
+    __builtin_amdgcn_sched_barrier(0);
     read(f0, 0, 0, 0, [](int) {});
   }
-  // One window: step 0 on f0 under the reads of step 1 into f1; the hand-over waits for window w+1 (only dy of window
-  // w+2 may still be in flight) and releases window w's slots; step 1 on f1 under the reads of window w+1's step 0 and the
-  // loads of x of window w+2 and dy of window w+3 into those slots.  CODES: x of window w+1 is written ahead of the
-  // hand-over, into the slot that the last one released, and the codes of window w+2 are loaded behind it.
+  // One window: step 0 on f0 under the reads of step 1 into f1; the hand-over waits for window w+1 and releases window w's
+  // slots; step 1 on f1 under the reads of window w+1's step 0 and the loads of dy of window w+NY into its slot.
+  // x of window w+1: CODES, written ahead of the hand-over into the slot that the last one released, whereupon the codes
+  // of window w+NY are loaded; else, loaded into LDS ahead of dy by the window before.
+  // In flight behind dy of window w+1 at the hand-over: dy of NY - 2 windows, and the codes of NY - 1.
+  constexpr int IN_FLIGHT = (NY - 2) * LY + (CODES ? (NY - 1) * 2 * UPT : 0);
+  static_assert(IN_FLIGHT < 64 && (CODES || NY == 3), "what the waits count");
   uint32_t sx = 0, sy = 0;
-  for (int w = w_lo; w < w_hi; ++w) {
+  auto window = [&](int w, auto i_tag) {
+    constexpr int NEXT = (decltype(i_tag)::value + 1) % D;
     const __amdgpu_buffer_rsrc_t rx = x_rows(w + NX), ry = y_rows(w + NY);
     const uint32_t sx1 = sx ^ 1, sy1 = sy == NY - 1 ? 0 : sy + 1;
     read(f1, sx, sy, 1, [](int) {});
     if constexpr (CODES) {
-      store_codes(raw, sx1);
-      raw = load_codes(w + 2);
+      store_codes(raw[NEXT], sx1);
+      raw[NEXT] = load_codes(w + NY);
     }
     step(f0);
     if constexpr (!CODES) grad_region<0, RD, MI * MJ, 0>(std::make_integer_sequence<int, RD>{});
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(grad_wait_vm(CODES ? LY + 2 : LY));
+    __builtin_amdgcn_s_waitcnt(grad_wait_vm(IN_FLIGHT));
     barrier();
     __builtin_amdgcn_sched_barrier(0);
     read(f0, sx1, sy1, 0, [&](int k) {
@@ -309,7 +339,20 @@ __global__ __launch_bounds__(64 * WK * WN, 1) void grad_weight_kernel(GradParams
     __builtin_amdgcn_sched_barrier(0);
     sx = sx1;
     sy = sy1;
-  }
+  };
+  // D windows at a time, so that the registers of codes on their way need not move; no way out between them, whose state
+  // the compiler would join with that of the next turn
+  int w = w_lo;
+  for (; w + D <= w_hi; w += D)
+    each_window<D>([&](auto i_tag) {
+      window(w + decltype(i_tag)::value, i_tag);
+      return true;
+    });
+  each_window<D>([&](auto i_tag) {
+    if (w + decltype(i_tag)::value >= w_hi) return false;
+    window(w + decltype(i_tag)::value, i_tag);
+    return true;
+  });
   // lane l holds columns k 4 (l / 16) .. + 3 of row n l % 16 of each block
   float* const sums = part >= 0 ? p.part + ((int64_t)(seq - p.whole) * p.splits + part) * (T::BN * T::BK) : nullptr;
 #pragma unroll
@@ -422,19 +465,18 @@ hipError_t launch_grad_weight_int8(const uint16_t* dy, int64_t ld_dy, const int8
   p.vec = reinterpret_cast<uintptr_t>(out) % (4 * step) == 0 && ld_out % 4 == 0;
   const int rest = g.tiles_n * g.tiles_k - g.whole;
   const unsigned grid = (unsigned)(g.whole + rest * g.splits);
-  auto go = [&](auto f_tag, auto c_tag, auto mi_tag, auto mj_tag) {
+  auto go = [&](auto f_tag, auto c_tag, auto tile) {
     constexpr bool F = decltype(f_tag)::value, C = decltype(c_tag)::value;
-    constexpr int MI = decltype(mi_tag)::value, MJ = decltype(mj_tag)::value;
-    using T = GradTile<MI, MJ, 4, 2>;
-    hipLaunchKernelGGL((grad_weight_kernel<F, C, MI, MJ, 4, 2>), dim3(grid), dim3(T::THREADS), 0, stream, p);
+    using T = decltype(tile);
+    hipLaunchKernelGGL((grad_weight_kernel<F, C, T>), dim3(grid), dim3(T::THREADS), 0, stream, p);
     if (rest > 0)
       hipLaunchKernelGGL((grad_weight_sums_kernel<F, T::BN, T::BK>), dim3(T::BN * T::BK / 1024, rest), dim3(256), 0, stream, p);
   };
   auto size = [&](auto f) {
     if (g.size == 256)
-      go(f, std::false_type{}, std::integral_constant<int, 4>{}, std::integral_constant<int, 8>{});
+      go(f, std::false_type{}, GradTile<4, 8, 4, 2, 3>{});
     else
-      go(f, std::true_type{}, std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
+      go(f, std::true_type{}, GradTile<4, 4, 2, 2, 3>{});
   };
   f32_out ? size(std::true_type{}) : size(std::false_type{});
   return hipGetLastError();
