@@ -469,7 +469,8 @@ mxq_status mxq_layer_norm(const void* x, mxq_dtype dt, int64_t rows, int64_t col
 /*
  * mxq_quantize_layer_norm -- the same, then the rule of mxq_quantize_int8 on the binary32 values of
  * each row: codes (pitch ld_codes bytes; base and pitch multiples of 16) and float scales[rows],
- * operands of mxq_gemm_w8a8.  cols: a multiple of 16.
+ * operands of mxq_gemm_w8a8.  A row whose squares overflow, or with eps == 0 of equal values, gets scale
+ * NaN and codes 0.  cols: a multiple of 16.
  */
 mxq_status mxq_quantize_layer_norm(const void* x, mxq_dtype dt, int64_t rows, int64_t cols, int64_t ld_x,
                                    const void* w, const void* b, mxq_dtype w_dt, float eps, int8_t* codes,

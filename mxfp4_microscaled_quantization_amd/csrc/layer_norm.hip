@@ -33,6 +33,11 @@ __device__ __forceinline__ void load_vector8(const void* w, int f32, uint32_t i,
   }
 }
 
+// Whether a row has 8-bit codes: not where its squares overflow or, without eps, vanish, nor where it has a NaN.
+__device__ __forceinline__ bool finite_stats(float var, float rstd) {
+  return var < __builtin_inff() && rstd < __builtin_inff();
+}
+
 // The sums of a wave over its elements of a row, as they are joined: with m the rounded mean of its elements and
 // d = x - m, e = sum d / n takes back what m lost in its rounding, and m2 = sum (d - e)^2.
 struct WaveSums {
@@ -183,7 +188,7 @@ __global__ __launch_bounds__(C == 4 || (C == 2 && !ONE) ? 512 : 256) void layer_
       }
     } else {
       // the largest magnitude by a floating maximum, which passes over a NaN: there is one only where a weight or
-      // bias is no number, or the statistics are not finite
+      // bias is not finite, or the statistics are not
       constexpr bool HOLD = C < 4;   // with 4 units the registers are short: the results are formed again
       float o[HOLD ? C : 1][8], most = 0.0f;
 #pragma unroll
@@ -194,7 +199,7 @@ __global__ __launch_bounds__(C == 4 || (C == 2 && !ONE) ? 512 : 256) void layer_
 #pragma unroll
           for (int k = 0; k < 8; k += 2) most = fmaxf(fmaxf(most, fabsf(v[k])), fabsf(v[k + 1]));
       }
-      unsigned top_y = group_max<64>(odd || !(var < __builtin_inff()) ? 0x7FC00000u : __float_as_uint(most));
+      unsigned top_y = group_max<64>(odd || !finite_stats(var, rstd) ? 0x7FC00000u : __float_as_uint(most));
       if constexpr (!ONE) {
         if (lane == 0) tops[par][1][wave] = top_y;
         __syncthreads();
@@ -263,7 +268,7 @@ __global__ __launch_bounds__(256) void layer_norm_short_kernel(NormParams p) {
           __builtin_nontemporal_store(unit_codes<F32>(u[k], sc), reinterpret_cast<v2u*>(p.kept + row * p.ld_kept + (int64_t)l * 8));
       }
       if constexpr (QUANT) {
-        const Int8Scale sc = int8_scale(group_max<G>(own ? max_abs8(v) : 0u));
+        const Int8Scale sc = int8_scale(group_max<G>(!finite_stats(var, rstd) ? 0x7FC00000u : own ? max_abs8(v) : 0u));
         if (l == 0 && there) p.scales[row] = sc.s;
         if (own && there)
           __builtin_nontemporal_store(pack_codes(v, sc), reinterpret_cast<v2u*>(static_cast<int8_t*>(p.y) + row * p.ld_y + (int64_t)l * 8));
@@ -282,7 +287,7 @@ template <bool F32, bool CODES> struct Kept { Unit<F32> u; };
 template <bool F32> struct Kept<F32, true> { v2u u; };
 
 // Threads of a workgroup: one for each unit of a row up to kNormThreads, U units for each beyond;
-// R rows at once.  AFFINE: with weights, and their sums.
+// R rows at once.  AFFINE: with weights or their sums.
 template <bool F32, bool CODES, bool AFFINE, int U, int R>
 __global__ __launch_bounds__(kNormThreads) void layer_norm_backward_kernel(NormGradParams p) {
   static_assert(R == 1 || R == 2, "the four rows of a wave's lanes hold the sums");
@@ -374,7 +379,7 @@ __global__ __launch_bounds__(kNormThreads) void layer_norm_backward_kernel(NormG
       }
     }
   }
-  if constexpr (AFFINE) {
+  if (AFFINE && p.dw) {
     float* part = p.part + (int64_t)blockIdx.x * 2 * p.units * 8;
 #pragma unroll
     for (int c = 0; c < U; ++c) {
@@ -443,7 +448,7 @@ __global__ __launch_bounds__(256) void layer_norm_backward_short_kernel(NormGrad
       if (in) store_unit<F32, true>(p.dx, row * p.ld_dx + (int64_t)l * 8, d);
     }
   }
-  if constexpr (AFFINE) {
+  if (AFFINE && p.dw) {
     // lanes of one l in a wave, then the waves
     auto over_groups = [](float v) {
       if constexpr (G == 8) v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xF, 0xF, true));   // row_ror by 8
@@ -583,9 +588,9 @@ size_t layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
 
 hipError_t launch_layer_norm_backward(const NormGradParams& p, bool f32, bool codes, hipStream_t stream) {
   const int64_t cols = (int64_t)p.units * 8;
-  const bool affine = p.dw != nullptr;
+  const bool sums = p.dw != nullptr, affine = sums || p.w;
   if (p.rows == 0) {
-    if (!affine) return hipSuccess;
+    if (!sums) return hipSuccess;
     hipLaunchKernelGGL(layer_norm_sums_kernel, dim3((unsigned)((2 * cols + 63) / 64)), dim3(1024), 0, stream, p.part, 0, (uint32_t)cols, p.dw, p.db);
     return hipGetLastError();
   }
@@ -614,7 +619,7 @@ hipError_t launch_layer_norm_backward(const NormGradParams& p, bool f32, bool co
   auto a = [&](auto f, auto c) { affine ? u(f, c, T{}) : u(f, c, N{}); };
   auto c = [&](auto f) { codes ? a(f, T{}) : a(f, N{}); };
   f32 ? c(T{}) : c(N{});
-  if (affine && groups > 1)
+  if (sums && groups > 1)
     hipLaunchKernelGGL(layer_norm_sums_kernel, dim3((unsigned)((2 * cols + 63) / 64)), dim3(1024), 0, stream, p.part,
                        (int)groups, (uint32_t)cols, p.dw, p.db);
   return hipGetLastError();

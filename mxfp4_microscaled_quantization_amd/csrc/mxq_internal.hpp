@@ -108,7 +108,7 @@ struct NormGradParams {
   const float *x_scales, *mean, *rstd;
   const void* w;           // or null
   void* dx;
-  float *dw, *db;          // both null: no weights
+  float *dw, *db;          // or both null
   float* part;             // sums of the workgroups
   int64_t rows, ld_dy, ld_x, ld_dx;
   uint32_t units;

@@ -210,3 +210,60 @@ def test_empty(gpu):
     assert y.shape == (0, 64) and mean.numel() == 0 and c.shape == (0, 64)
     dx, dw, db = gpu.layer_norm_backward(x, x, mean, rstd, torch.ones(64, device="cuda"))
     assert dx.shape == (0, 64) and not dw.any() and not db.any() and dw.shape == (64,)
+
+
+@pytest.mark.parametrize("T,C", [(5, 96), (3, 1040), (7, 4112), (2, 9008), (1100, 272)])
+def test_sums_and_weights_apart(gpu, T, C):
+    """Through the C ABI: weights without their sums, and sums without weights (weights of 1)."""
+    announce(f"layer_norm_backward apart {T}x{C}")
+    g = torch.Generator().manual_seed(T)
+    x, dy, w = _rows(g, T, C, F32), _rows(g, T, C, F32), torch.randn(C, generator=g).cuda()
+    _, mean, rstd = gpu.layer_norm(x, save="x")
+    ptr = lambda t: None if t is None else t.data_ptr()   # noqa: E731
+    nbytes = gpu.lib.mxq_layer_norm_backward_workspace_bytes(T, C)
+    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device="cuda")
+
+    def call(w, dw, db):
+        dx = torch.empty_like(x)
+        st = gpu.lib.mxq_layer_norm_backward(ptr(dy), 0, T, C, C, ptr(x), C, None, ptr(mean), ptr(rstd), ptr(w), 0, ptr(dx), C, ptr(dw), ptr(db),
+                                             ptr(ws), nbytes, torch.cuda.current_stream().cuda_stream)
+        assert st == 0, gpu.lib.mxq_last_error()
+        return dx
+
+    full, dw, db = gpu.layer_norm_backward(dy, x, mean, rstd, w)
+    assert torch.equal(call(w, None, None), full)
+    ones, sw, sb = torch.ones(C, device="cuda"), torch.empty(C, device="cuda"), torch.empty(C, device="cuda")
+    plain = call(None, sw, sb)
+    assert torch.equal(plain, gpu.layer_norm_backward(dy, x, mean, rstd, ones)[0]) and torch.equal(sw, dw) and torch.equal(sb, db)
+    assert torch.equal(plain, gpu.layer_norm_backward(dy, x, mean, rstd)[0])
+
+
+@pytest.mark.parametrize("C", [64, 512, 1360, 5120, 13824])
+def test_rows_without_finite_statistics(gpu, C):
+    """Squares past binary32, and equal values without eps: NaN scales and codes of 0 in the quantized form, other
+    rows as they are alone."""
+    announce(f"layer_norm statistics {C}")
+    g = torch.Generator().manual_seed(C)
+    x = _rows(g, 6, C, F32)
+    clean, cs = gpu.quantize_layer_norm(x, eps=0.0)
+    x[1], x[4] = x[1] * 1e30, 3.0
+    codes, s = gpu.quantize_layer_norm(x, eps=0.0)
+    y = gpu.layer_norm(x, eps=0.0)
+    assert y[4].isnan().all() and s[[1, 4]].isnan().all() and not codes[[1, 4]].any()
+    keep = [0, 2, 3, 5]
+    assert torch.equal(codes[keep], clean[keep]) and torch.equal(s[keep], cs[keep])
+
+
+def test_weights_that_are_not_numbers(gpu):
+    """A NaN or an infinity in a weight or bias reaches its column of every row: the rows' scales are NaN."""
+    announce("layer_norm bad weights")
+    for C in (64, 528, 1040, 5120, 13824):
+        x = torch.randn(3, C, device="cuda")
+        for bad in (float("nan"), float("inf")):
+            for which in (0, 1):
+                v = [torch.ones(C, device="cuda"), torch.zeros(C, device="cuda")]
+                v[which][C - 3] = bad
+                codes, s = gpu.quantize_layer_norm(x, *v)
+                y = gpu.layer_norm(x, *v)
+                cols = torch.arange(C, device="cuda") != C - 3
+                assert s.isnan().all() and not codes.any() and not y[:, C - 3].isfinite().any() and y[:, cols].isfinite().all()
