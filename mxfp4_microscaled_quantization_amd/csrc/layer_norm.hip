@@ -47,8 +47,8 @@ struct WaveSums {
 // A row over the whole workgroup of 4 or 8 waves (a multiple of the 4 SIMDs), or (ONE) over a wave, four rows in a workgroup and nothing
 // synchronized; C units of 8 elements in each thread.  A workgroup takes many rows: it keeps its columns'
 // weights, and loads its next row while it works on one.
-template <bool F32, bool QUANT, int C, bool ONE>
-__global__ __launch_bounds__(C == 4 || (C == 2 && !ONE) ? 512 : 256) void layer_norm_kernel(NormParams p) {
+template <bool F32, bool QUANT, int C, bool ONE, int MOST = 256>
+__global__ __launch_bounds__(MOST) void layer_norm_kernel(NormParams p) {
   // two slots in turn: a wave may reach the next row's store while another still reads
   __shared__ WaveSums sums[2][16];
   __shared__ unsigned tops[2][2][16];
@@ -90,14 +90,21 @@ __global__ __launch_bounds__(C == 4 || (C == 2 && !ONE) ? 512 : 256) void layer_
 #pragma unroll
   for (int c = 0; c < C; ++c) u[c] = next[c] = zero_unit<F32>();   // threads past the row
   if (row < p.rows) load_row(row, u);
-  float w[C][8], b[C][8];
+  // With 4 units the registers are short.  In bf16 the weights are read for each row, from the caches (30000 x 13824 to
+  // codes 297 us, held 328); in binary32 they are held, and codes are formed from results computed again (378 us, read 457).
+  constexpr bool HELD = C < 4 || F32, HOLD = C < 4 || !F32;
+  float w[HELD ? C : 1][8], b[HELD ? C : 1][8];
+  auto load_weights = [&](int c) {
+    const uint32_t i = c * T + tid;
+    load_vector8(i < p.units ? p.w : nullptr, p.w_f32, i, 1.0f, w[HELD ? c : 0]);
+    load_vector8(i < p.units ? p.b : nullptr, p.w_f32, i, 0.0f, b[HELD ? c : 0]);
+  };
   bool odd = false;   // an infinity or a NaN among them
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const uint32_t i = c * T + tid;
-    load_vector8(i < p.units ? p.w : nullptr, p.w_f32, i, 1.0f, w[c]);
-    load_vector8(i < p.units ? p.b : nullptr, p.w_f32, i, 0.0f, b[c]);
-    odd |= max(max_abs8(w[c]), max_abs8(b[c])) >= 0x7F800000u;
+    if (!HELD && !QUANT) break;
+    load_weights(c);
+    odd |= max(max_abs8(w[HELD ? c : 0]), max_abs8(b[HELD ? c : 0])) >= 0x7F800000u;
   }
   for (int par = 0; row < p.rows; row += stride, par ^= 1) {
     if (row + stride < p.rows) load_row(row + stride, next);
@@ -169,8 +176,10 @@ __global__ __launch_bounds__(C == 4 || (C == 2 && !ONE) ? 512 : 256) void layer_
     auto result = [&](int c, float(&o)[8]) {
       forget_unit<F32>(u[c]);
       widen_unit<F32>(u[c], o);
+      if constexpr (!HELD) load_weights(c);
+      const float(&wc)[8] = w[HELD ? c : 0], (&bc)[8] = b[HELD ? c : 0];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = __builtin_fmaf(__builtin_fmaf(o[k] - mean, rstd, shift), w[c][k], b[c][k]);
+      for (int k = 0; k < 8; ++k) o[k] = __builtin_fmaf(__builtin_fmaf(o[k] - mean, rstd, shift), wc[k], bc[k]);
     };
     char* y = static_cast<char*>(p.y) + row * p.ld_y * (QUANT ? 1 : F32 ? 4 : 2);
     if constexpr (!QUANT) {
@@ -189,7 +198,6 @@ __global__ __launch_bounds__(C == 4 || (C == 2 && !ONE) ? 512 : 256) void layer_
     } else {
       // the largest magnitude by a floating maximum, which passes over a NaN: there is one only where a weight or
       // bias is not finite, or the statistics are not
-      constexpr bool HOLD = C < 4;   // with 4 units the registers are short: the results are formed again
       float o[HOLD ? C : 1][8], most = 0.0f;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
@@ -570,9 +578,11 @@ hipError_t launch_layer_norm(const NormParams& args, bool f32, bool quant, hipSt
     else if (p.units <= 256 * 3)
       go(layer_norm_kernel<F, Q, 3, false>, 256, 1, most);
     else if (p.units <= 512 * 2)
-      go(layer_norm_kernel<F, Q, 2, false>, 512, 1, most);
+      go(layer_norm_kernel<F, Q, 2, false, 512>, 512, 1, most);
+    else if (p.units <= 512 * 3)
+      go(layer_norm_kernel<F, Q, 3, false, 512>, 512, 1, most);
     else
-      go(layer_norm_kernel<F, Q, 4, false>, 512, 1, most);
+      go(layer_norm_kernel<F, Q, 4, false, 512>, 512, 1, most);
   };
   using T = std::true_type;
   using N = std::false_type;
