@@ -99,13 +99,15 @@ __global__ __launch_bounds__(64 * (W < 4 ? 4 : W)) void activation_kernel(ActPar
     for (int c = 0; c < C; ++c) {
       const uint32_t i = c * T + tid;
       float(&o)[8] = y[QUANT ? c : 0];
-      widen_unit<F32>(u[c], o);
+      if (i < p.units) {   // a wave past the row has nothing to compute
+        widen_unit<F32>(u[c], o);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = act<ACT>(o[e]);
-      if constexpr (QUANT)
-        most = max8(most, o);
-      else if (i < p.units)
-        store_unit<F32, STREAM>(p.y, row * p.ld_y + (int64_t)i * 8, o);
+        for (int e = 0; e < 8; ++e) o[e] = act<ACT>(o[e]);
+        if constexpr (QUANT)
+          most = max8(most, o);
+        else
+          store_unit<F32, STREAM>(p.y, row * p.ld_y + (int64_t)i * 8, o);
+      }
       top_u = max(top_u, unit_max<F32>(u[c]));
     }
     if (QUANT || p.kept) {
