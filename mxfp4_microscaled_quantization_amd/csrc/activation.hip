@@ -240,6 +240,19 @@ hipError_t launch_activation(const ActParams& p, bool f32, bool quant, ActKind a
   auto pick = [&](auto f_tag, auto s_tag, auto q_tag, auto a_tag) {
     constexpr bool F = decltype(f_tag)::value, S = decltype(s_tag)::value, Q = decltype(q_tag)::value;
     constexpr int A = decltype(a_tag)::value;
+    auto longest = [&] {
+      if (p.units <= 1024 * 4)
+        go(activation_kernel<F, S, Q, A, 16, 4>, 1024, 1);
+      else
+        go(activation_kernel<F, S, Q, A, 16, 8>, 1024, 1);
+    };
+    // The waves of a row, us at 13824 columns and more rows than the GPU holds unless said otherwise.  Up to 32 units several
+    // rows share a wave (150000 x 256 bf16 to codes 24, a wave for each row 39).  A row's codes wait in registers for its
+    // scales, which every wave has to work out: few waves of longer threads (75600 rows bf16 557, over 16 waves 872; 40000 x
+    // 2048 38, over 4 waves 46).  A result that is stored at once has nothing to wait for: more waves, in binary32 of one
+    // unit a thread as far as that goes (30000 x 4096 174, over 4 waves 185), in bf16, whose codes beside the result
+    // are packed for each wave, of three from 4096 to 6144 columns and from 8192 to 12288 (20000 x 4112 with codes 73, of two 88;
+    // plain 55 and 55) and of two or one elsewhere (40000 x 2048 52, over one wave 60; 20000 x 6160 86, of four 90).
     if (p.units <= 8)
       go(activation_short_kernel<F, S, Q, A, 8>, 256, 32 * 4);
     else if (p.units <= 16)
@@ -252,27 +265,48 @@ hipError_t launch_activation(const ActParams& p, bool f32, bool quant, ActKind a
       go(activation_kernel<F, S, Q, A, 1, 2>, 256, 4);
     else if (p.units <= 192)
       go(activation_kernel<F, S, Q, A, 1, 3>, 256, 4);
-    else if (p.units <= 256)
-      go(activation_kernel<F, S, Q, A, 1, 4>, 256, 4);
-    else if (p.units <= 256 * 2)
-      go(activation_kernel<F, S, Q, A, 4, 2>, 256, 1);
-    else if (p.units <= 256 * 3)
-      go(activation_kernel<F, S, Q, A, 4, 3>, 256, 1);
-    else if (p.units <= 256 * 4)
-      go(activation_kernel<F, S, Q, A, 4, 4>, 256, 1);
-    else if (p.units <= 512 * 3)
-      go(activation_kernel<F, S, Q, A, 8, 3>, 512, 1);
-    else if (p.units <= 1024 * 2) {
-      // a row's values stay in registers where they become codes: fewer and longer threads then (75600 x 13824 bf16 to
-      // codes: 591 us, over 16 waves 872; to bf16 with a checkpoint 914 and 897)
-      if constexpr (Q)
+    else if constexpr (Q) {
+      if (p.units <= 256)
+        go(activation_kernel<F, S, Q, A, 1, 4>, 256, 4);
+      else if (p.units <= 256 * 2)
+        go(activation_kernel<F, S, Q, A, 4, 2>, 256, 1);
+      else if (p.units <= 256 * 3)
+        go(activation_kernel<F, S, Q, A, 4, 3>, 256, 1);
+      else if (p.units <= 256 * 4)
+        go(activation_kernel<F, S, Q, A, 4, 4>, 256, 1);
+      else if (p.units <= 512 * 3)
+        go(activation_kernel<F, S, Q, A, 8, 3>, 512, 1);
+      else if (p.units <= 512 * 4)
         go(activation_kernel<F, S, Q, A, 8, 4>, 512, 1);
       else
+        longest();
+    } else if constexpr (F) {
+      if (p.units <= 256)
+        go(activation_kernel<F, S, Q, A, 4, 1>, 256, 1);
+      else if (p.units <= 512)
+        go(activation_kernel<F, S, Q, A, 8, 1>, 512, 1);
+      else if (p.units <= 512 * 2)
+        go(activation_kernel<F, S, Q, A, 8, 2>, 512, 1);
+      else if (p.units <= 1024 * 2)
         go(activation_kernel<F, S, Q, A, 16, 2>, 1024, 1);
-    } else if (p.units <= 1024 * 4)
-      go(activation_kernel<F, S, Q, A, 16, 4>, 1024, 1);
-    else
-      go(activation_kernel<F, S, Q, A, 16, 8>, 1024, 1);
+      else
+        longest();
+    } else {
+      if (p.units <= 256)
+        go(activation_kernel<F, S, Q, A, 4, 1>, 256, 1);
+      else if (p.units <= 256 * 2)
+        go(activation_kernel<F, S, Q, A, 4, 2>, 256, 1);
+      else if (p.units <= 256 * 3)
+        go(activation_kernel<F, S, Q, A, 4, 3>, 256, 1);
+      else if (p.units <= 512 * 2)
+        go(activation_kernel<F, S, Q, A, 8, 2>, 512, 1);
+      else if (p.units <= 512 * 3)
+        go(activation_kernel<F, S, Q, A, 8, 3>, 512, 1);
+      else if (p.units <= 1024 * 2)
+        go(activation_kernel<F, S, Q, A, 16, 2>, 1024, 1);
+      else
+        longest();
+    }
   };
   // see launch_quantize_int8
   const bool stream_loads = p.rows * (int64_t)p.units * 8 * (f32 ? 4 : 2) > ((int64_t)256 << 20);
