@@ -6,13 +6,16 @@
 // from it (DPP and lane swaps); the waves' means, counts and squares are then joined through LDS
 // behind one barrier, sum_k m2_k + n_k (m_k - mean)^2, which is a sum of squares again: nothing cancels.
 // What a mean loses in its rounding is taken from the deviations.  A row is read once and
-// stays in registers as it was loaded.  Bound by HBM.
+// stays in registers as it was loaded.  Bound by HBM: 75600 x 5120 bf16 273 us (5.7 TB/s; a 1 GiB copy reaches 5.0),
+// with the kept codes 348 (5.6), binary32 567 (5.5), 30000 x 13824 bf16 350 (4.7: one workgroup on a CU).  To codes the
+// vector units are never idle either: 228 us (5.1 TB/s).
 //
 // Backward, with xh = (x - mean) * rstd and g = dy * w:
 //   dx = rstd * (g - sum g / C - xh * sum (g xh) / C),  dw = sum_rows dy xh,  db = sum_rows dy
 // x is the kept input, or its 8-bit codes and row scales.  A thread owns 8 U columns for all
 // the rows that its workgroup takes, so that dw and db stay in its registers; the workgroups'
-// sums are joined by a second kernel in a fixed order.
+// sums are joined by a second kernel in a fixed order.  Bound by HBM: 75600 x 5120 bf16 399 us (5.8 TB/s), from codes
+// 327 (5.9), 30000 x 13824 436 (5.7); rows of a thousand elements wait for their sums (60000 x 1040 83 us, 4.5 TB/s).
 #include <type_traits>
 
 #include "mxq_internal.hpp"
@@ -514,7 +517,8 @@ __global__ __launch_bounds__(1024) void layer_norm_sums_kernel(const float* part
   }
 }
 
-// The gradient's launch.  Workgroups leave 2 C floats each, so that there are no more of them than the GPU runs at once,
+// The gradient's launch.  Several rows share a wave up to 64 units (80000 x 512 bf16 49 us, a workgroup of one wave 65).
+// Workgroups leave 2 C floats each, so that there are no more of them than the GPU runs at once,
 // and each has 8 rows or more where there are enough rows (4099 x 2064 binary32: 512 workgroups 26 us, 1024 33, 256 30;
 // 75600 x 5120 bf16 from codes: 512 328 us, 1024 392).
 struct GradLaunch {
@@ -549,9 +553,9 @@ hipError_t launch_layer_norm(const NormParams& args, bool f32, bool quant, hipSt
   NormParams p = args;
   // see launch_quantize_int8
   p.past = p.rows * (int64_t)p.units * 8 * (f32 ? 4 : 2) > ((int64_t)256 << 20);
-  // `rows_each` rows in turn for a workgroup where there are enough.  Their weights cost it a reading of the caches
+  // About 6 rows in turn for a workgroup where there are enough.  Their weights cost it a reading of the caches
   // once, but workgroups that stay for all rows are slower than ones that come and go: 75600 x 5120 bf16 with 1 row
-  // each 354 us, 2 295, 5 276, 9 284, 18 296, 74 295.
+  // each 354 us, 2 295, 5 276, 6 274, 9 284, 18 296, 74 295.
   auto go = [&](auto kernel, int threads, int rows_per_block, int64_t most) {
     const int64_t sets = (p.rows + rows_per_block - 1) / rows_per_block;
     const int64_t few = 256 * (2048 / threads), many = sets / 6;
@@ -561,6 +565,10 @@ hipError_t launch_layer_norm(const NormParams& args, bool f32, bool quant, hipSt
   auto pick = [&](auto f_tag, auto q_tag) {
     constexpr bool F = decltype(f_tag)::value, Q = decltype(q_tag)::value;
     const int64_t most = (int64_t)1 << 20;   // blocks * threads stays below 2^32
+    // us, to bf16 and to codes.  Several rows in a wave up to 32 units (150000 x 256 26 and 28, a wave for each row 33 and
+    // 45; 80000 x 272, one row in a wave, 21 and 28), one wave for a row up to 192 (40000 x 1536 38 and 31, a workgroup
+    // 42 and 57), then a workgroup of 4 waves up to 768 units, of 8 beyond (20000 x 5120 78 and 60, of 8 waves 80 and
+    // 78), so that a thread holds 4 units at most.
     if (p.units <= 8)
       go(layer_norm_short_kernel<F, Q, 8>, 256, 32 * 4, most);
     else if (p.units <= 16)
