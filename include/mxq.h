@@ -1,6 +1,7 @@
 /*
  * mxq.h -- C ABI of libmxq: OCP MXFP4 block quantization and the W4A4 / W4A8 GEMMs that
- * consume it, with a bf16 reference GEMM and whole-output SQNR, for AMD Instinct MI355X
+ * consume it, with a bf16 reference GEMM and whole-output SQNR; 8-bit products and the operators
+ * between them, with backward passes from activations kept in 8 bits; for AMD Instinct MI355X
  * (gfx950).
  *
  * Sources (web pages, cited by title and section):
