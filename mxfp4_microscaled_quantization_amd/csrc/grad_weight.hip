@@ -413,7 +413,8 @@ GradPlan plan_grad(int64_t M, int64_t N, int64_t K) {
     const int64_t whole = tiles / slots * slots, rest = tiles - whole;
     // the largest tile's operand is widened by a launch of its own
     const double base = (double)(whole / slots) * (nwin * window + ends) + (size == 256 ? 4.0 + (double)M * K * 3 / 5.5e6 : 0.0);
-    for (int s = 1; s == 1 || (s * 2 <= nwin && rest * s <= 4 * slots); ++s) {
+    // every number of parts up to 32, then steps of 1 in 32, for the host's time (75600 x 128 x 128: 7.5 us, so 2.8)
+    for (int s = 1; s == 1 || (s * 2 <= nwin && rest * s <= 4 * slots); s += 1 + s / 32) {
       double t = base;
       if (rest > 0) {
         t += (double)((rest * s + slots - 1) / slots) * ((nwin + s - 1) / s * window + ends);
