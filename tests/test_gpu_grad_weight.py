@@ -128,3 +128,21 @@ def test_empty(gpu):
     have = torch.ones(24, 32, device="cuda")
     assert gpu.grad_weight_int8(e(0, 24).bfloat16(), e(0, 32).to(torch.int8), e(0), out=have, accumulate=True).eq(1).all()
     assert gpu.grad_weight_int8(e(5, 0).bfloat16(), e(5, 32).to(torch.int8), e(5)).shape == (0, 32)
+
+
+@pytest.mark.parametrize("M,N,K", [(2300, 136, 400), (9001, 264, 144), (30001, 136, 16), (24000, 1288, 272), (70000, 8, 48)])
+def test_many_parts_of_few_tiles(gpu, M, N, K):
+    """Sums cut into more than 16 parts of M, which several threads of the joining kernel share."""
+    announce(f"grad_weight_int8 parts {M}x{N}x{K}")
+    assert gpu.lib.mxq_grad_weight_int8_workspace_bytes(M, N, K) > 16 * 128 * 128 * 4
+    dy, codes, s = _inputs(M, N, K, M + K, 8)
+    ref, size = tr.grad_weight_int8(_np(dy), codes.cpu().numpy(), s.cpu().numpy())
+    out = gpu.grad_weight_int8(dy, codes, s)
+    _check(out, ref, size)
+    assert torch.equal(out, gpu.grad_weight_int8(dy, codes, s))
+    assert torch.equal(gpu.grad_weight_int8(dy, codes, s, out_dtype=BF16), out.bfloat16())
+    have = torch.randn(N, K + 8, device="cuda")
+    wide = have.clone()
+    gpu.grad_weight_int8(dy, codes, s, out=wide[:, 1:K + 1], accumulate=True)
+    _check(wide[:, 1:K + 1], ref + _np(have[:, 1:K + 1]), size, 2.0 ** -23 * (np.abs(_np(have[:, 1:K + 1])) + np.abs(ref)))
+    assert torch.equal(wide[:, 0], have[:, 0]) and torch.equal(wide[:, K + 1:], have[:, K + 1:])
