@@ -408,6 +408,8 @@ __global__ __launch_bounds__(256) void grad_weight_sums_kernel(GradParams p) {
 // Which tile, and how the tiles share the GPU: as many whole rounds of it as there are, and the rest of the
 // tiles cut into parts of M.  Times in us.  Measured, tokens x N x K:
 //                         256-wide  128-wide    not cut
+//   64 x 13824 x 5120           64        56         56
+//   700 x 3000 x 3008           33        30         30
 //   2000 x 1024 x 1024          32        25         28
 //   4096 x 2048 x 2048          55        55         55
 //   16384 x 1024 x 640          48        41        177
@@ -423,17 +425,23 @@ GradPlan plan_grad(int64_t M, int64_t N, int64_t K) {
   const int nwin = (int)((M + kWinRows - 1) / kWinRows);
   for (const int size : {256, 128}) {
     const int64_t slots = size == 256 ? 256 : 512;                  // workgroups at once
-    const double window = size == 256 ? 1.65 : 1.15, ends = 6.0;    // of a workgroup on a full GPU
+    const double window = size == 256 ? 1.65 : 1.15;                // of a workgroup on a full GPU,
+    const double alone = size == 256 ? 1.65 : 0.72;                 // and with a CU to itself
+    const double ends = size == 256 ? 10.0 : 5.0;                   // first loads, last stores
     const int64_t tn = (N + size - 1) / size, tk = (K + size - 1) / size, tiles = tn * tk;
     const int64_t whole = tiles / slots * slots, rest = tiles - whole;
+    auto rounds = [&](int64_t n, int windows) {                     // of n workgroups
+      const int64_t full = n / slots, left = n - full * slots;
+      return (double)full * (windows * window + ends) + (left > 0 ? windows * (left <= 256 ? alone : window) + ends : 0.0);
+    };
     // the largest tile's operand is widened by a launch of its own
-    const double base = (double)(whole / slots) * (nwin * window + ends) + (size == 256 ? 4.0 + (double)M * K * 3 / 5.5e6 : 0.0);
+    const double base = rounds(whole, nwin) + (size == 256 ? 4.0 + (double)M * K * 3 / 5.5e6 : 0.0);
     // every number of parts up to 32, then steps of 1 in 32, for the host's time (75600 x 128 x 128: 7.5 us, so 2.8)
     for (int s = 1; s == 1 || (s * 2 <= nwin && rest * s <= 4 * slots); s += 1 + s / 32) {
       double t = base;
       if (rest > 0) {
-        t += (double)((rest * s + slots - 1) / slots) * ((nwin + s - 1) / s * window + ends);
-        if (s > 1) t += 5.0 + (double)(rest * s * size * size) * 8.0 / 5.5e6;
+        t += rounds(rest * s, (nwin + s - 1) / s);
+        if (s > 1) t += 5.0 + (double)(rest * s * size * size) * 4.0 / 5.5e6;
       }
       if (least == 0.0 || t < least) {
         least = t;
