@@ -50,7 +50,8 @@ __device__ __forceinline__ float act(float u) {
 // f' = s + u s (1 - s) z', with 1 - s = e s: no difference of nearly equal numbers
 template <int ACT>
 __device__ __forceinline__ float act_slope(float u) {
-  const float e = exp_minus_z<ACT>(u), s = __builtin_amdgcn_rcpf(1.0f + e);
+  // e stays finite, so that the limit far below is 0
+  const float e = fminf(exp_minus_z<ACT>(u), 0x1p100f), s = __builtin_amdgcn_rcpf(1.0f + e);
   const float t = ACT == ACT_GELU_TANH ? u * __builtin_fmaf(u * u, kGeluDz2, kGeluDz) : u;
   return __builtin_fmaf(t * (e * s), s, s);
 }

@@ -163,3 +163,17 @@ def test_empty(gpu):
     assert y.shape == c.shape == (0, 64) and s.shape == (0,) and gpu.activation_backward(y, c, s).shape == (0, 64)
     z = torch.zeros(3, 0, dtype=BF16, device="cuda")
     assert gpu.activation(z).shape == (3, 0)
+
+
+@pytest.mark.parametrize("act", ["gelu_tanh", "silu"])
+def test_slope_far_beyond_the_checkpoint(gpu, act):
+    """Scales that no checkpoint has: the derivative goes to its limits, 0 and 1, and never to NaN."""
+    announce(f"activation_backward far values {act}")
+    codes = torch.tensor([-128, -127, -100, 0, 100, 126, 127, 127] * 2, dtype=torch.int8, device="cuda").repeat(5, 1)
+    scales = torch.tensor([0.5, 1.0, 16.0, 100.0, 1e4], device="cuda")
+    slope = gpu.activation_backward(torch.ones(5, 16, device="cuda"), codes, scales, act)
+    v = codes.float() * scales[:, None]
+    assert torch.equal(v < 0, codes < 0) and bool((v.abs()[codes != 0] >= 50).all())
+    # beyond 50 the distance from a limit is under 51 exp(-50), less than a step of binary32
+    want = torch.where(v > 0, 1.0, torch.where(v < 0, 0.0, 0.5))
+    assert bool(((slope - want).abs() <= 2.0 ** -23).all())
