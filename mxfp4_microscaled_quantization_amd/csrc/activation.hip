@@ -110,7 +110,7 @@ __global__ __launch_bounds__(64 * (W < 4 ? 4 : W)) void activation_kernel(ActPar
         if constexpr (QUANT)
           most = max8(most, o);
         else
-          store_unit<F32, STREAM>(p.y, row * p.ld_y + (int64_t)i * 8, o);
+          store_out<F32, STREAM>(p.y, row * p.ld_y + (int64_t)i * 8, o, (i | 3) < p.units);
       }
       top_u = max(top_u, unit_max<F32>(u[c]));
     }
@@ -185,7 +185,7 @@ __global__ __launch_bounds__(256) void activation_short_kernel(ActParams p) {
         if (in)
           __builtin_nontemporal_store(pack_codes(o, sc), reinterpret_cast<v2u*>(static_cast<int8_t*>(p.y) + row * p.ld_y + (int64_t)l * 8));
       } else if (in) {
-        store_unit<F32, STREAM>(p.y, row * p.ld_y + (int64_t)l * 8, o);
+        store_out<F32, STREAM>(p.y, row * p.ld_y + (int64_t)l * 8, o, (l | 3) < p.units);
       }
       if (p.kept) {
         const Int8Scale sc = checkpoint_scale<ACT>(top_u);
@@ -227,7 +227,8 @@ __global__ __launch_bounds__(kActGradThreads) void activation_backward_kernel(Ac
       widen_unit<F32>(d[k], o);
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] *= act_slope<ACT>(v[e]);
-      if (ok[k]) store_unit<F32, true>(p.dx, row[k] * p.ld_dx + col[k], o);
+      // whole quads of units in each row (60000 x 1040, of 130 units: 106 us, quad by quad 111)
+      if (ok[k]) store_out<F32, true>(p.dx, row[k] * p.ld_dx + col[k], o, p.units % 4 == 0);
     }
   }
 }

@@ -193,7 +193,7 @@ __global__ __launch_bounds__(MOST) void layer_norm_kernel(NormParams p) {
           float o[8];
           result(c, o);
           if (p.past)
-            store_unit<F32, true>(y, i * 8, o);
+            store_out<F32, true>(y, i * 8, o, (i | 3) < p.units);
           else
             store_unit<F32, false>(y, i * 8, o);
         }
@@ -285,7 +285,7 @@ __global__ __launch_bounds__(256) void layer_norm_short_kernel(NormParams p) {
           __builtin_nontemporal_store(pack_codes(v, sc), reinterpret_cast<v2u*>(static_cast<int8_t*>(p.y) + row * p.ld_y + (int64_t)l * 8));
       } else if (own && there) {
         if (p.past)
-          store_unit<F32, true>(p.y, row * p.ld_y + (int64_t)l * 8, v);
+          store_out<F32, true>(p.y, row * p.ld_y + (int64_t)l * 8, v, (l | 3) < p.units);
         else
           store_unit<F32, false>(p.y, row * p.ld_y + (int64_t)l * 8, v);
       }
@@ -386,7 +386,7 @@ __global__ __launch_bounds__(kNormThreads) void layer_norm_backward_kernel(NormG
         float o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = rstd[r] * (g[r][c][e] - __builtin_fmaf(xh[r][c][e], c2, c1));
-        if (i < p.units) store_unit<F32, true>(dx_row, i * 8, o);
+        if (i < p.units) store_out<F32, true>(dx_row, i * 8, o, (i | 3) < p.units);
       }
     }
   }
@@ -456,7 +456,7 @@ __global__ __launch_bounds__(256) void layer_norm_backward_short_kernel(NormGrad
       const float c1 = group_sum<G>(s1) * p.inv_cols, c2 = group_sum<G>(s2) * p.inv_cols;
 #pragma unroll
       for (int e = 0; e < 8; ++e) d[e] = rstd[r] * (d[e] - __builtin_fmaf(xh[e], c2, c1));
-      if (in) store_unit<F32, true>(p.dx, row * p.ld_dx + (int64_t)l * 8, d);
+      if (in) store_out<F32, true>(p.dx, row * p.ld_dx + (int64_t)l * 8, d, (l | 3) < p.units);
     }
   }
   if (AFFINE && p.dw) {

@@ -177,3 +177,19 @@ def test_slope_far_beyond_the_checkpoint(gpu, act):
     # beyond 50 the distance from a limit is under 51 exp(-50), less than a step of binary32
     want = torch.where(v > 0, 1.0, torch.where(v < 0, 0.0, 0.5))
     assert bool(((slope - want).abs() <= 2.0 ** -23).all())
+
+
+@pytest.mark.parametrize("C", [72, 264, 1032, 1048, 2056, 4104, 9224])
+def test_large_rows_past_the_caches(gpu, C):
+    """Inputs over 256 MB are stored past the caches, in runs of 4 lanes where a row has them: the bits of small ones."""
+    announce(f"large binary32 rows of {C}")
+    T = (300 << 20) // (4 * C) + 3
+    x = torch.randn(T, C, device="cuda")
+    w = torch.rand(C, device="cuda") + 0.5
+    for run in (lambda t: gpu.activation(t, "silu"), lambda t: gpu.layer_norm(t, w)):
+        whole = run(x)
+        for r in range(0, T, T // 3):
+            part = slice(r, min(r + T // 3, T))
+            assert torch.equal(whole[part], run(x[part]))
+    y = x.clone()
+    assert torch.equal(gpu.activation(y, "silu", out=y), gpu.activation(x, "silu")) and y.shape == x.shape
