@@ -7,7 +7,7 @@
 // behind one barrier, sum_k m2_k + n_k (m_k - mean)^2, which is a sum of squares again: nothing cancels.
 // What a mean loses in its rounding is taken from the deviations.  A row is read once and
 // stays in registers as it was loaded.  Bound by HBM: 75600 x 5120 bf16 273 us (5.7 TB/s; a 1 GiB copy reaches 5.0),
-// with the kept codes 348 (5.6), binary32 567 (5.5), 30000 x 13824 bf16 350 (4.7: one workgroup on a CU).  To codes the
+// with the kept codes 348 (5.6), binary32 562 (5.5), 30000 x 13824 bf16 350 (4.7: one workgroup on a CU).  To codes the
 // vector units are never idle either: 228 us (5.1 TB/s).
 //
 // Backward, with xh = (x - mean) * rstd and g = dy * w:
@@ -15,7 +15,7 @@
 // x is the kept input, or its 8-bit codes and row scales.  A thread owns 8 U columns for all
 // the rows that its workgroup takes, so that dw and db stay in its registers; the workgroups'
 // sums are joined by a second kernel in a fixed order.  Bound by HBM: 75600 x 5120 bf16 399 us (5.8 TB/s), from codes
-// 327 (5.9), 30000 x 13824 436 (5.7); rows of a thousand elements wait for their sums (60000 x 1040 83 us, 4.5 TB/s).
+// 327 (5.9), binary32 877 (5.3), 30000 x 13824 bf16 436 (5.7); rows of a thousand elements wait for their sums (60000 x 1040 83 us, 4.5 TB/s).
 #include <type_traits>
 
 #include "mxq_internal.hpp"
@@ -540,7 +540,7 @@ GradLaunch grad_launch(int64_t rows, int64_t cols) {
 
 // Whether a workgroup takes two rows at once, with one barrier for both: where a row has few waves (60000 x 1040 bf16 from
 // codes: 75 us for 80), where the GPU holds but one workgroup on a CU (30000 x 8192: 226 us for 243), and for binary32
-// (75600 x 5120: 917 us for 956).  Not for the rows between, of which more fit the registers one by one (75600 x
+// (75600 x 5120: 877 us for 918).  Not for the rows between, of which more fit the registers one by one (75600 x
 // 5120 bf16 from codes: 371 us for 328).
 bool two_rows(int64_t rows, int threads, bool f32) {
   return rows >= 1024 && (f32 || threads <= 256 || threads > 768);
