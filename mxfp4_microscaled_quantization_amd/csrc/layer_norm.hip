@@ -115,7 +115,7 @@ __global__ __launch_bounds__(MOST) void layer_norm_kernel(NormParams p) {
     float s = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) s = sum_unit<F32>(u[c], s);
-    const float m = wave_sum(s) * inv_n;
+    const float m = rounded_product(wave_sum(s), inv_n);
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -253,7 +253,7 @@ __global__ __launch_bounds__(256) void layer_norm_short_kernel(NormParams p) {
       const bool there = row < p.rows;
       float v[8];
       widen_unit<F32>(u[k], v);
-      const float m = group_sum<G>(sum_unit<F32>(u[k], 0.0f)) * p.inv_cols;
+      const float m = rounded_product(group_sum<G>(sum_unit<F32>(u[k], 0.0f)), p.inv_cols);
       float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {

@@ -185,6 +185,12 @@ __device__ __forceinline__ float sum_unit(const Unit<F32>& u, float s) {
   }
 }
 
+// a * b as a binary32 value, the same wherever it is used: not contracted into one of the sums that it is a part of.
+__device__ __forceinline__ float rounded_product(float a, float b) {
+#pragma clang fp contract(off)
+  return a * b;
+}
+
 // s / n, rounded correctly but for rare last bits, from inv = fl32(1 / n); exact where n divides s.
 __device__ __forceinline__ float quotient(float s, float n, float inv) {
   const float q = s * inv;

@@ -1,0 +1,47 @@
+"""Layer norm where its statistics could lose digits: rows of equal values, and means far from zero, at every width."""
+
+import pytest
+import torch
+
+from oracle import training as tr
+from helpers import announce
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+# rows that share a wave, a wave a row, 4 and 8 waves; counts that binary32 divides exactly and others
+WIDTHS = [8, 24, 40, 64, 72, 120, 200, 248, 256, 264, 504, 776, 1016, 1360, 1536, 1544, 2040, 3000, 4104, 5120, 6136, 6152, 8192, 9000, 13824, 16376, 16384]
+
+
+@pytest.mark.parametrize("C", WIDTHS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_equal_values_are_the_bias(gpu, dtype, C):
+    """Deviations of 0 from a mean that is the value itself, whatever the rounding of 1 / C: b, to the last bit."""
+    announce(f"layer_norm equal values {C} {dtype}")
+    g = torch.Generator("cuda").manual_seed(C)
+    size = torch.exp(3 * torch.randn(400, 1, device="cuda", generator=g))
+    x = (torch.randn(400, 1, device="cuda", generator=g) * size).to(dtype).expand(400, C).contiguous()
+    w, b = torch.randn(C, device="cuda", generator=g), torch.randn(C, device="cuda", generator=g)
+    y, mean, rstd = gpu.layer_norm(x, w, b, eps=1e-6, save="x")
+    assert torch.equal(mean, x[:, 0].float()) and bool(((rstd - 1e3).abs() <= 1e3 * 2.0 ** -22).all())
+    assert torch.equal(y, b.to(dtype).expand_as(y))
+    if C % 16:
+        return
+    codes, s = gpu.quantize_layer_norm(x, w, b, eps=1e-6)
+    want, ws = gpu.quantize_int8(b[None])
+    assert torch.equal(codes, want.expand_as(codes)) and torch.equal(s, ws.expand_as(s))
+
+
+@pytest.mark.parametrize("C", WIDTHS)
+def test_means_far_from_zero(gpu, C):
+    """Deviations of a few last digits of the mean: they are exact in binary32, so that y is as near as anywhere
+    (the bounds of test_gpu_layer_norm)."""
+    announce(f"layer_norm far means {C}")
+    g = torch.Generator().manual_seed(C)
+    far = torch.exp(4 * torch.rand(64, 1, generator=g)) * 100
+    x = (far + torch.randn(64, C, generator=g) * far * 2.0 ** -18).cuda()
+    ref, m, r, size = tr.layer_norm(x.double().cpu().numpy(), None, None, 1e-12)
+    y, mean, rstd = gpu.layer_norm(x, eps=1e-12, save="x")
+    assert bool((abs(y.double().cpu().numpy() - ref) <= 2.0 ** -18 * size + 2.0 ** -24 * abs(ref)).all())
+    assert bool((abs(rstd.double().cpu().numpy() - r) <= 2.0 ** -18 * r).all())
+    assert bool((abs(mean.double().cpu().numpy() - m) <= 2.0 ** -23 * abs(m) + 2.0 ** -18 / r).all())
