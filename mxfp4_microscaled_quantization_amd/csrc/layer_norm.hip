@@ -47,6 +47,33 @@ struct WaveSums {
   float m, e, m2;
 };
 
+// The sums of a row whose squares came out past binary32, once more over G lanes, `in(c)` telling which units are there.  Of large equal
+// values the sum overflows, or their rounded mean is off by a last digit whose square does: here the sum is taken of
+// values times 2^-11 (G lanes have up to 2^11 of them), the mean kept finite, and the squares taken of what is left once e is off too:
+// 0 for equal values.  Deviations that do have such squares, an infinity or a NaN come out as they did.
+template <bool F32, int C, int G, class In>
+__device__ __forceinline__ WaveSums large_sums(Unit<F32> (&u)[C], float n, float inv_n, In in) {
+  static_assert(C * G <= 256, "2^11 values");
+  auto sum = [&](auto value) {
+    float s = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      forget_unit<F32>(u[c]);
+      if (in(c)) {
+        float v[8];
+        widen_unit<F32>(u[c], v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s += value(v[k]);
+      }
+    }
+    return group_sum<G>(s);
+  };
+  constexpr float kTop = 0x1.fffffep127f;
+  const float m = __builtin_amdgcn_fmed3f(sum([](float x) { return x * 0x1p-11f; }) * inv_n * 0x1p11f, -kTop, kTop);
+  const float e = quotient(sum([&](float x) { return x - m; }), n, inv_n);
+  return WaveSums{m, e, sum([&](float x) { const float d = (x - m) - e; return d * d; })};
+}
+
 // A row over the whole workgroup of 4 or 8 waves (a multiple of the 4 SIMDs), or (ONE) over a wave, four rows in a workgroup and nothing
 // synchronized; C units of 8 elements in each thread.  A workgroup takes many rows: it keeps its columns'
 // weights, and loads its next row while it works on one.
@@ -115,7 +142,7 @@ __global__ __launch_bounds__(MOST) void layer_norm_kernel(NormParams p) {
     float s = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) s = sum_unit<F32>(u[c], s);
-    const float m = rounded_product(wave_sum(s), inv_n);
+    float m = rounded_product(wave_sum(s), inv_n);
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -134,7 +161,13 @@ __global__ __launch_bounds__(MOST) void layer_norm_kernel(NormParams p) {
     s1 = of_lane(pair, 0);
     s2 = of_lane(pair, 32);
     // quotients, not products with a rounded 1 / n: a row of equal values then has deviations of exactly 0
-    const float e = quotient(s1, n, inv_n), q = __builtin_fmaf(-s1, e, s2);
+    float e = quotient(s1, n, inv_n), q = __builtin_fmaf(-s1, e, s2);
+    if (!(q < __builtin_inff())) {   // the whole wave
+      const WaveSums k = large_sums<F32, C, 64>(u, n, inv_n, [&](int c) { return c * T + tid < p.units; });
+      m = k.m;
+      e = k.e;
+      q = k.m2;
+    }
     unsigned top = 0;
     if (p.kept) {
 #pragma unroll
@@ -231,9 +264,10 @@ __global__ __launch_bounds__(MOST) void layer_norm_kernel(NormParams p) {
 }
 
 // Rows of up to G units, 64 / G of them in a wave: lane l of a group has unit l, R rows of each
-// group in flight, the weights in registers.
+// group in flight, the weights in registers.  Registers for 4 waves on a SIMD: the compiler then spreads the rows in flight over them
+// (300000 x 128 fp32 with kept codes 65 us, for 5 waves 69; bf16 33 either way).
 template <bool F32, bool QUANT, int G>
-__global__ __launch_bounds__(256) void layer_norm_short_kernel(NormParams p) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 4))) void layer_norm_short_kernel(NormParams p) {
   constexpr int PER = 256 / G, R = 4;   // rows of the workgroup at once, passes in flight
   const uint32_t l = threadIdx.x % G;
   const bool own = l < p.units;
@@ -247,24 +281,11 @@ __global__ __launch_bounds__(256) void layer_norm_short_kernel(NormParams p) {
       const int64_t row = r0 + k * PER;
       u[k] = own && row < p.rows ? (p.past ? load_unit<F32, true>(p.x, row * p.ld_x + (int64_t)l * 8) : load_unit<F32, false>(p.x, row * p.ld_x + (int64_t)l * 8)) : zero_unit<F32>();
     }
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
+    auto put = [&](int k, float mean, float rest, float m2) {
       const int64_t row = r0 + k * PER;
       const bool there = row < p.rows;
       float v[8];
       widen_unit<F32>(u[k], v);
-      const float m = rounded_product(group_sum<G>(sum_unit<F32>(u[k], 0.0f)), p.inv_cols);
-      float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = own ? v[e] - m : 0.0f;
-        s1 += d;
-        s2 = __builtin_fmaf(d, d, s2);
-      }
-      s1 = group_sum<G>(s1);
-      s2 = group_sum<G>(s2);
-      const float e0 = quotient(s1, p.cols, p.inv_cols), m2 = __builtin_fmaf(-s1, e0, s2);
-      const float mean = m + e0, rest = (m - mean) + e0;
       const float var = m2 == m2 ? fmaxf(m2, 0.0f) * p.inv_cols : m2, rstd = rsqrtf(var + p.eps);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(__builtin_fmaf(v[e] - mean, rstd, -rest * rstd), w[e], b[e]);
@@ -289,6 +310,37 @@ __global__ __launch_bounds__(256) void layer_norm_short_kernel(NormParams p) {
         else
           store_unit<F32, false>(p.y, row * p.ld_y + (int64_t)l * 8, v);
       }
+    };
+    // rows for large_sums, of any group: they are written again, so that the others wait for no branch of theirs
+    unsigned large = 0;
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      float v[8];
+      widen_unit<F32>(u[k], v);
+      const float m = rounded_product(group_sum<G>(sum_unit<F32>(u[k], 0.0f)), p.inv_cols);
+      float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = own ? v[e] - m : 0.0f;
+        s1 += d;
+        s2 = __builtin_fmaf(d, d, s2);
+      }
+      s1 = group_sum<G>(s1);
+      s2 = group_sum<G>(s2);
+      const float e0 = quotient(s1, p.cols, p.inv_cols), m2 = __builtin_fmaf(-s1, e0, s2);
+      const float mean = m + e0;
+      put(k, mean, (m - mean) + e0, m2);
+      large |= m2 < __builtin_inff() ? 0u : 1u << k;
+    }
+    if (large) {
+#pragma unroll
+      for (int k = 0; k < R; ++k)
+        if (large >> k & 1) {
+          Unit<F32> one[1] = {u[k]};
+          const WaveSums t = large_sums<F32, 1, G>(one, p.cols, p.inv_cols, [&](int) { return own; });
+          const float mean = t.m + t.e;
+          put(k, mean, (t.m - mean) + t.e, t.m2);
+        }
     }
   }
 }

@@ -45,3 +45,42 @@ def test_means_far_from_zero(gpu, C):
     assert bool((abs(y.double().cpu().numpy() - ref) <= 2.0 ** -18 * size + 2.0 ** -24 * abs(ref)).all())
     assert bool((abs(rstd.double().cpu().numpy() - r) <= 2.0 ** -18 * r).all())
     assert bool((abs(mean.double().cpu().numpy() - m) <= 2.0 ** -23 * abs(m) + 2.0 ** -18 / r).all())
+
+
+@pytest.mark.parametrize("C", WIDTHS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_large_equal_values_are_the_bias(gpu, dtype, C):
+    """Also where the sum of the row, or the square of a last digit of its values, is past binary32."""
+    announce(f"layer_norm large equal values {C} {dtype}")
+    top = torch.finfo(dtype).max
+    values = [top, -top, top * (1 - 2.0 ** -7), 2.0 ** 127, -(2.0 ** 120), 1e37, 3e30, -7e27, 1e26, 2.0 ** 118, 3.0, -1e-30]
+    x = torch.tensor(values).to(dtype).cuda()[:, None].repeat(12, C)
+    w, b = torch.randn(C, device="cuda"), torch.randn(C, device="cuda")
+    y, mean, rstd = gpu.layer_norm(x, w, b, eps=1e-6, save="x")
+    assert torch.equal(mean, x[:, 0].float()) and bool(((rstd - 1e3).abs() <= 1e3 * 2.0 ** -22).all())
+    assert torch.equal(y, b.to(dtype).expand_as(y))
+    if C % 16:
+        return
+    codes, s = gpu.quantize_layer_norm(x, w, b, eps=1e-6)
+    want, ws = gpu.quantize_int8(b[None])
+    assert torch.equal(codes, want.expand_as(codes)) and torch.equal(s, ws.expand_as(s))
+
+
+@pytest.mark.parametrize("C", [64, 240, 248, 1360, 5120, 16384])
+def test_rows_beside_large_ones(gpu, C):
+    """Large equal values, an infinity and deviations without squares in binary32 among ordinary rows, whose bits stay."""
+    announce(f"layer_norm beside large rows {C}")
+    x = torch.randn(101, C, device="cuda")
+    clean = gpu.layer_norm(x, save="x")
+    x[::10], x[5::20], x[7::20, C // 2] = 3e38, torch.randn(C, device="cuda") * 1e30, float("inf")
+    got = gpu.layer_norm(x, save="x")
+    plain = torch.ones(101, dtype=torch.bool, device="cuda")
+    plain[::10] = plain[5::20] = plain[7::20] = False
+    assert all(torch.equal(a[plain], b[plain]) for a, b in zip(got, clean))
+    assert not got[0][::10].any() and bool((got[1][::10] == x[0, 0]).all()) and got[0][7::20].isnan().all()
+    y = x.clone()
+    assert torch.equal(gpu.layer_norm(y, out=y).nan_to_num(1e9), got[0].nan_to_num(1e9))
+    if C % 16:
+        return
+    codes, s = gpu.quantize_layer_norm(x)
+    assert s[5::20].isnan().all() and s[7::20].isnan().all() and not s[::10].any() and s[plain].isfinite().all()
