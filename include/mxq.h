@@ -541,7 +541,8 @@ mxq_status mxq_quantize_activation(const void* u, mxq_dtype dt, int64_t rows, in
  * mxq_activation_backward -- du = dy * f'(v) with v = fl32(code * scale) of the checkpoint, in
  * binary32, rounded to `dt` once.
  * dy, du  : rows x cols of `dt`, pitches in elements, 16-byte aligned; du may be dy with the same pitch.
- * u_codes, u_scales : the checkpoint of the same activation.  cols: a multiple of 16.
+ * u_codes, u_scales : the checkpoint of the same activation (or any other codes and scales; a row whose scale is
+ *           not finite gives NaN).  cols: a multiple of 16.
  */
 mxq_status mxq_activation_backward(const void* dy, mxq_dtype dt, int64_t rows, int64_t cols, int64_t ld_dy,
                                    const int8_t* u_codes, int64_t ld_uc, const float* u_scales,

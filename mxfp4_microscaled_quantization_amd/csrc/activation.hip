@@ -47,13 +47,19 @@ __device__ __forceinline__ float act(float u) {
   return u * __builtin_amdgcn_rcpf(1.0f + exp_minus_z<ACT>(u));
 }
 
-// f' = s + u s (1 - s) z', with 1 - s = e s: no difference of nearly equal numbers
+// f' = s + u s (1 - s) z', with 1 - s = e s: no difference of nearly equal numbers.  For |u| up to 2^14 (slope_scale).
 template <int ACT>
 __device__ __forceinline__ float act_slope(float u) {
-  // e stays finite, so that the limit far below is 0
+  // e stays finite, so that the limit far below is 0 within 2^45 2^-100: u z' s (1 - s) grows as u^3 at most
   const float e = fminf(exp_minus_z<ACT>(u), 0x1p100f), s = __builtin_amdgcn_rcpf(1.0f + e);
   const float t = ACT == ACT_GELU_TANH ? u * __builtin_fmaf(u * u, kGeluDz2, kGeluDz) : u;
   return __builtin_fmaf(t * (e * s), s, s);
+}
+
+// The scale of a row of codes for its slopes: clamped to +-128, where a code other than 0 is past the end of the slope's way to
+// its limits (at 128 already for the nearest code), and u, up to 2^14, is where act_slope is good.  NaN where it is not finite.
+__device__ __forceinline__ float slope_scale(float s) {
+  return fabsf(s) < __builtin_inff() ? __builtin_amdgcn_fmed3f(s, -128.0f, 128.0f) : __uint_as_float(0x7FC00000u);
 }
 
 // Largest |v| by a floating maximum, which passes over a NaN.  The values are finite where u is (|f(u)| <= |u|), and a row
@@ -223,7 +229,7 @@ __global__ __launch_bounds__(kActGradThreads) void activation_backward_kernel(Ac
 #pragma unroll
     for (int k = 0; k < kActGradUnroll; ++k) {
       float v[8], o[8];
-      widen_codes(c[k], s[k], v);
+      widen_codes(c[k], slope_scale(s[k]), v);
       widen_unit<F32>(d[k], o);
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] *= act_slope<ACT>(v[e]);
