@@ -808,12 +808,13 @@ def quantize_layer_norm(x, weight=None, bias=None, eps=1e-6, save=None):
     return (codes, scales, *saved)
 
 
-def layer_norm_backward(dy, x, mean, rstd, weight=None, x_scales=None, out=None):
-    """Gradient of layer_norm: (dx, dweight, dbias), the last two float32 [C] and None without ``weight``.
+def layer_norm_backward(dy, x, mean, rstd, weight=None, x_scales=None, out=None, sums=None):
+    """Gradient of layer_norm: (dx, dweight, dbias), the last two float32 [C], or None where they are not formed.
 
     ``dy`` [T, C], bf16 or fp32; ``x``: the forward input, of dy's type, or its int8 codes with ``x_scales``
     (save="int8").  ``mean``, ``rstd``: float32 [T] of the forward pass.  dx has dy's type; ``out=dy`` works in place.
-    The sums over rows are formed in a fixed order."""
+    ``sums``: whether dweight and dbias are formed, by default where there is a ``weight``; True for a norm with a
+    bias alone, False where the weights are not trained.  The sums over rows are formed in a fixed order."""
     ld = _matrix(dy, "dy", _FLOATS)
     dev, (R, C) = dy.device, dy.shape
     if x_scales is not None:
@@ -825,7 +826,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, x_scales=None, out=None)
     dx, ldo = _plane(out, "out", dy.dtype, R, C, dev)
     dw = db = ws = None
     nbytes = 0
-    if weight is not None:
+    if weight is not None if sums is None else sums:
         dw, db = _row_values(C, dev), _row_values(C, dev)
         nbytes = lib.mxq_layer_norm_backward_workspace_bytes(R, C)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
