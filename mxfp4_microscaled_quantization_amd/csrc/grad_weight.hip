@@ -344,7 +344,10 @@ __global__ __launch_bounds__(T::THREADS, 2) void grad_weight_kernel(GradParams p
     sy = sy1;
   };
   // D windows at a time, so that the registers of codes on their way need not move; no way out between them, whose state
-  // the compiler would join with that of the next turn
+  // the compiler would join with that of the next turn.  The codes that a window of the tail loads are not used, and the compiler leaves
+  // the loads out: its hand-over waits for fewer loads than IN_FLIGHT counts on, and dy of the window behind it may
+  // not have landed.  No window reads that dy, as long as the tail is one window, the last.
+  static_assert(!CODES || D <= 2, "a tail of more windows needs waits of its own");
   int w = w_lo;
   for (; w + D <= w_hi; w += D)
     each_window<D>([&](auto i_tag) {
