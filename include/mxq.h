@@ -482,8 +482,8 @@ mxq_status mxq_quantize_layer_norm(const void* x, mxq_dtype dt, int64_t rows, in
  * mxq_layer_norm_backward -- with xh = (x - mean) * rstd and g = dy * w, in binary32:
  *   dx = rstd * ( g - sum g / cols - xh * sum (g xh) / cols ), rounded to `dt` once;
  *   dw = sum over rows of dy * xh;  db = sum over rows of dy.
- * The sums over rows are formed in an order that rows, cols, dt and the kind of x decide: the same
- * inputs give the same bits.
+ * The sums over rows are formed in an order that rows, cols and dt alone decide: the same inputs
+ * give the same bits.
  * dy, dx  : rows x cols of `dt`; dx may be dy with the same pitch.
  * x       : with x_scales NULL the kept input, of `dt`; else its codes (int8, one float x_scales
  *           for each row; cols a multiple of 16), which stand for fl32(code * scale).
