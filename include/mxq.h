@@ -450,10 +450,12 @@ mxq_status mxq_quantize_qk_norm_rope(const void* q, int64_t heads_q, int64_t ld_
  * mxq_layer_norm -- for each row x of cols elements, in binary32:
  *   mean = sum x / cols;  rstd = 1 / sqrt( sum (x - mean)^2 / cols + eps );
  *   y = (x - mean) * rstd * w + b,  rounded to `dt` once.
- * The deviations are taken from the mean itself (no difference of two squares).  A row with an
- * infinity or a NaN comes out as NaN; a row whose squares overflow binary32 (deviations of
- * 2^60 and more) as b, infinities or NaN; with eps == 0 a row of equal values as NaN.  Other
- * rows are unaffected.
+ * The deviations are taken from the mean itself (no difference of two squares), and a row of equal
+ * finite values comes out as b.  A row with an infinity or a NaN comes out as NaN; a row whose squared
+ * deviations overflow binary32 in their sum (a root mean square of 2^64 / sqrt(cols) and more) as b,
+ * infinities or NaN.  With eps == 0 a row of equal values is NaN, and deviations that are all below 2^-60 lose
+ * digits, for their squares leave binary32's normal numbers (all below 2^-75: infinities or NaN).
+ * Other rows are unaffected.
  * x       : rows x cols of `dt`, pitch ld_x elements; base and pitch 16-byte aligned.
  * w, b    : cols weights and biases of w_dt, 16-byte aligned; either may be NULL (1, 0).
  * y       : out, rows x cols of `dt`, pitch ld_y elements; base and pitch 16-byte aligned.  May be
@@ -470,7 +472,7 @@ mxq_status mxq_layer_norm(const void* x, mxq_dtype dt, int64_t rows, int64_t col
 /*
  * mxq_quantize_layer_norm -- the same, then the rule of mxq_quantize_int8 on the binary32 values of
  * each row: codes (pitch ld_codes bytes; base and pitch multiples of 16) and float scales[rows],
- * operands of mxq_gemm_w8a8.  A row whose squares overflow, or with eps == 0 of equal values, gets scale
+ * operands of mxq_gemm_w8a8.  A row whose squares overflow, or with eps == 0 vanish, gets scale
  * NaN and codes 0.  cols: a multiple of 16.
  */
 mxq_status mxq_quantize_layer_norm(const void* x, mxq_dtype dt, int64_t rows, int64_t cols, int64_t ld_x,

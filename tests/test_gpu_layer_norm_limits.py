@@ -84,3 +84,33 @@ def test_rows_beside_large_ones(gpu, C):
         return
     codes, s = gpu.quantize_layer_norm(x)
     assert s[5::20].isnan().all() and s[7::20].isnan().all() and not s[::10].any() and s[plain].isfinite().all()
+
+
+@pytest.mark.parametrize("C", WIDTHS)
+def test_range_of_the_deviations(gpu, C):
+    """Without eps a power of two comes out of y exactly, from deviations of 2^-60 up to where the sum of their squares
+    nears 2^128: the bits of deviations around 1."""
+    announce(f"layer_norm range of deviations {C}")
+    g = torch.Generator("cuda").manual_seed(C)
+    x = torch.randn(65, C, device="cuda", generator=g).clamp(-4, 4)
+    # at least 2^-5 off the mean on the whole, at most 4: sums of squares below 2^4 C
+    y, mean, rstd = gpu.layer_norm(x, eps=0.0, save="x")
+    top = int(62 - torch.tensor(float(C)).log2().ceil().item() / 2)
+    for e in (-55, -30, 30, top - 4, top - 3):
+        y2, mean2, rstd2 = gpu.layer_norm(x * 2.0 ** e, eps=0.0, save="x")
+        assert torch.equal(y2, y) and torch.equal(mean2, mean * 2.0 ** e) and torch.equal(rstd2, rstd * 2.0 ** -e), e
+
+
+@pytest.mark.parametrize("C", [64, 248, 1360, 5120, 16384])
+def test_outside_the_range(gpu, C):
+    """Squares that overflow, or vanish without eps: y is b, infinite or NaN, and the quantized form's scale NaN."""
+    announce(f"layer_norm outside the range {C}")
+    x = torch.randn(3, C, device="cuda")
+    x[0] *= 2.0 ** 70
+    x[1] *= 2.0 ** -85
+    y = gpu.layer_norm(x, eps=0.0)
+    assert not (y[0].isfinite() & (y[0] != 0)).any() and not (y[1].isfinite() & (y[1] != 0)).any() and y[2].isfinite().all()
+    if C % 16:
+        return
+    codes, s = gpu.quantize_layer_norm(x, eps=0.0)
+    assert s[:2].isnan().all() and not codes[:2].any() and s[2].isfinite()
