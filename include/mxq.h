@@ -463,6 +463,8 @@ mxq_status mxq_quantize_qk_norm_rope(const void* q, int64_t heads_q, int64_t ld_
  * mean, rstd : out, float[rows] each, or both NULL.
  * x_codes, x_scales : out, the checkpoint mxq_quantize_int8(x), bit for bit (pitch ld_xc bytes, base
  *           and pitch multiples of 16), or x_codes NULL for none (ld_xc and x_scales are then ignored).
+ *           Their step is 1/127 of the row's largest |x|: (x - mean) * rstd from them is off by up to x_scales / 2 *
+ *           rstd, which is much for a row with an outlier or with a mean that is large beside its deviation.
  * cols    : a multiple of 8 (16 with x_codes), 8 to 16384.  eps finite and >= 0.
  */
 mxq_status mxq_layer_norm(const void* x, mxq_dtype dt, int64_t rows, int64_t cols, int64_t ld_x, const void* w,

@@ -792,7 +792,8 @@ def layer_norm(x, weight=None, bias=None, eps=1e-6, save=None, out=None):
 
     ``weight``, ``bias``: [C], bf16 or fp32, either None.  ``save``: what the backward pass needs, from the same
     pass over x: "x" returns (y, mean, rstd), to be kept with x itself; "int8" (C a multiple of 16) returns
-    (y, mean, rstd, x_codes, x_scales), the last two equal to quantize_int8(x).  ``out=x`` works in place."""
+    (y, mean, rstd, x_codes, x_scales), the last two equal to quantize_int8(x): half the bytes or less, for a gradient whose
+    normalized x is off by up to x_scales / 2 * rstd (much for a row with an outlier or a far mean).  ``out=x`` works in place."""
     args, saved, saved_args = _norm_inputs(x, weight, bias, eps, save)
     y, ld = _plane(out, "out", x.dtype, *x.shape, x.device)
     _call(lib.mxq_layer_norm, x.device, *args, y.data_ptr(), ld, *saved_args)

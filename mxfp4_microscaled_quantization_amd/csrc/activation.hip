@@ -13,9 +13,9 @@
 // Both are bound by HBM, with the vector units close behind (about 20 operations for each
 // element, two of them transcendental).  The forward pass holds a row in registers between its
 // maxima and its codes, as the row quantizer does; the backward pass is a plain element kernel.
-// 75600 x 13824 bf16, gelu_tanh: 690 us (6.1 TB/s), with a checkpoint 892 (5.9), to codes 557 (5.6, the vector units
-// never idle), to codes with a checkpoint 728 (5.7), backward 880 (5.9); a 1 GiB copy reaches 5.0 TB/s.  silu, which
-// has fewer operations, to codes 547.
+// 75600 x 13824 bf16, gelu_tanh: 687 us (6.1 TB/s), with a checkpoint 891 (5.9), to codes 560 (5.6, the vector units
+// never idle), to codes with a checkpoint 735 (5.7), backward 885 (5.9); a 1 GiB copy reaches 5.0 TB/s.  silu, which
+// has fewer operations, to codes 546.
 #include <type_traits>
 
 #include "mxq_internal.hpp"

@@ -10,8 +10,8 @@
 // come from LDS by ds_read_b64_tr_b16, in which 16 lanes read 4 rows of 16 columns and each
 // gets the 4 values of one column.
 //
-// Bound by the matrix cores, whose clock gives way first: 75600 tokens, 13824 x 5120 to binary32 8.25 ms, 1.30 PFLOP/s,
-// the product itself 7.95 with the matrix cores 75 % busy at 1.6 GHz (a library product of this layout on bf16
+// Bound by the matrix cores, whose clock gives way first: 75600 tokens, 13824 x 5120 to binary32 8.25 ms, 1.30 PFLOP/s (9.0 on
+// another card), the product itself 7.95 with the matrix cores 75 % busy at 1.6 GHz (a library product of this layout on bf16
 // operands that are there already: 10.5 ms; a square one of 8192 reaches 1.37 PFLOP/s with rows along the contraction).
 #include <type_traits>
 #include <utility>

@@ -6,16 +6,17 @@
 // from it (DPP and lane swaps); the waves' means, counts and squares are then joined through LDS
 // behind one barrier, sum_k m2_k + n_k (m_k - mean)^2, which is a sum of squares again: nothing cancels.
 // What a mean loses in its rounding is taken from the deviations.  A row is read once and
-// stays in registers as it was loaded.  Bound by HBM: 75600 x 5120 bf16 273 us (5.7 TB/s; a 1 GiB copy reaches 5.0),
-// with the kept codes 348 (5.6), binary32 562 (5.5), 30000 x 13824 bf16 350 (4.7: one workgroup on a CU).  To codes the
-// vector units are never idle either: 228 us (5.1 TB/s).
+// stays in registers as it was loaded.  Bound by HBM: 75600 x 5120 bf16 274 us (5.65 TB/s; a 1 GiB copy reaches 5.0),
+// with the kept codes 348 (5.6), binary32 565 (5.5), 30000 x 13824 bf16 339 (4.9), binary32 592 (5.6).  To codes the
+// vector units are never idle either, and time goes with the clock: 228 to 238 us (4.9 to 5.1 TB/s) at 2.4 GHz, 300 in the first
+// passes after a pause, at 2.0.
 //
 // Backward, with xh = (x - mean) * rstd and g = dy * w:
 //   dx = rstd * (g - sum g / C - xh * sum (g xh) / C),  dw = sum_rows dy xh,  db = sum_rows dy
 // x is the kept input, or its 8-bit codes and row scales.  A thread owns 8 U columns for all
 // the rows that its workgroup takes, so that dw and db stay in its registers; the workgroups'
-// sums are joined by a second kernel in a fixed order.  Bound by HBM: 75600 x 5120 bf16 399 us (5.8 TB/s), from codes
-// 327 (5.9), binary32 877 (5.3), 30000 x 13824 bf16 436 (5.7); rows of a thousand elements wait for their sums (60000 x 1040 83 us, 4.5 TB/s).
+// sums are joined by a second kernel in a fixed order.  Bound by HBM: 75600 x 5120 bf16 401 us (5.8 TB/s), from codes
+// 327 (5.9), binary32 880 (5.3), 30000 x 13824 bf16 437 (5.7); rows of a thousand elements wait for their sums (60000 x 1040 84 us, 4.5 TB/s).
 #include <type_traits>
 
 #include "mxq_internal.hpp"
