@@ -771,6 +771,8 @@ def _norm_vectors(weight, bias, cols, device):
 def _checkpoint(rows, cols, device):
     """New codes and scales: (tensors, C arguments)."""
     codes, scales = _empty((rows, cols), (cols, 1), dtype=torch.int8, device=device), _row_values(rows, device)
+    if cols == 0:   # no address of codes, which asks for no checkpoint: the scales of nothing are 0
+        scales.zero_()
     return (codes, scales), (codes.data_ptr(), cols, scales.data_ptr())
 
 

@@ -35,3 +35,18 @@ def test_scales_that_are_not_finite(gpu, act):
     du = gpu.activation_backward(torch.ones(6, 48, device="cuda"), codes, scales, act)
     assert du[[1, 3, 4]].isnan().all() and du[[0, 2, 5]].isfinite().all()
     assert torch.equal(du[[0, 2, 5]], gpu.activation_backward(torch.ones(3, 48, device="cuda"), codes[[0, 2, 5]], scales[[0, 2, 5]], act))
+
+
+def test_rows_of_no_columns(gpu):
+    """Their scales are 0, as quantize_int8's are, and not what the memory held."""
+    announce("activation no columns")
+    for dtype in (BF16, F32):
+        u = torch.zeros(5, 0, dtype=dtype, device="cuda")
+        for run, at in ((lambda: gpu.activation(u, save="int8"), (2,)), (lambda: gpu.quantize_activation(u, save="int8"), (1, 3)),
+                        (lambda: gpu.quantize_activation(u), (1,)), (lambda: gpu.quantize_int8(u), (1,))):
+            held = [torch.full((5,), 7.0, device="cuda") for _ in range(8)]
+            del held
+            out = run()
+            assert all(out[k].shape == (5,) and not out[k].any() for k in at)
+        y, codes, s = gpu.activation(u, save="int8")
+        assert gpu.activation_backward(y, codes, s).shape == (5, 0)
